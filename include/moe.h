@@ -146,6 +146,13 @@ int moe_bucket(const moe_ctx *ctx, const int32_t *ids_in, int32_t T, int32_t *co
                int32_t *offsets, int32_t *perm, void *workspace, size_t ws_bytes,
                hipStream_t stream);
 
+/* moe_bucket that also writes the inverse of perm: rows [T*8], rows[p] = the position of pair p in
+ * perm, i.e. its row among the pairs sorted by expert, or -1 for a dropped pair. rows is what the
+ * row operators below take. */
+int moe_bucket_rows(const moe_ctx *ctx, const int32_t *ids_in, int32_t T, int32_t *counts,
+                    int32_t *offsets, int32_t *perm, int32_t *rows, void *workspace,
+                    size_t ws_bytes, hipStream_t stream);
+
 /* The whole layer: y [T][H] fp32 from x [T][H].
  * Routing: ids_in, w_in, gate_in all NULL -> routed internally from x (as moe_route);
  * otherwise ids_in [T][8] (values in [0, E)) and w_in [T][8] are used as given (gate_in [T]
@@ -182,6 +189,71 @@ int moe_forward_timed(const moe_ctx *ctx, const void *x, int32_t T, const int32_
                       const float *w_in, const float *gate_in, float *y, void *workspace,
                       size_t ws_bytes, hipStream_t stream, hipEvent_t *events,
                       int32_t n_events);
+
+/* ---- Separate operators around a caller's own expert products --------------------------------
+ *
+ * They need no context and no workspace, keep nothing between calls and can be captured in a HIP
+ * graph. The current device must be the one that the stream and the pointers belong to. Row
+ * types are MOE_F32 or MOE_BF16 (another one: MOE_ERR_INVALID_ARG). Pointers to rows are 16-byte
+ * aligned, to rows/weights/scales/offsets 4-byte; matrices are row-major without gaps. Inputs and
+ * outputs of one call must not overlap. T: 0..1048576 tokens, H: 8..16384, a multiple of 8.
+ *
+ * rows [T*8] int32 (moe_bucket_rows): pair 8t + k of token t lives in row rows[8t + k] of the
+ * buffers sorted by expert, which hold n_rows rows (0..8388608, the caller's capacity). A pair
+ * whose entry lies outside [0, n_rows) is dropped: it is neither read nor written and adds nothing.
+ * Entries inside must be distinct (the tables of a bucketing are). Rows of an output that no
+ * pair names are left as they were. Sums run in rank order in fp32, rounded once to the output
+ * type (nearest, ties to even): a token's bits do not depend on the other tokens. */
+
+/* xs[rows[8t + k]] = x[t]: x [T][H] and xs [n_rows][H], both of `dtype`. */
+int moe_permute(const void *x, const int32_t *rows, int32_t T, int32_t H, int32_t n_rows,
+                int32_t dtype, void *xs, hipStream_t stream);
+
+/* Its gradient, dx[t] = sum_k dxs[rows[8t + k]] (0 for a token without kept pairs). */
+int moe_permute_backward(const void *dxs, const int32_t *rows, int32_t T, int32_t H,
+                         int32_t n_rows, int32_t dtype, void *dx, hipStream_t stream);
+
+/* y[t] = sum_k w[t][k] ys[rows[8t + k]] + gate[t] shared[t]: ys [n_rows][H] and shared [T][H] of
+ * `dtype`, w [T][8] and gate [T] fp32, y [T][H] of `y_dtype`. shared and gate: both or neither. */
+int moe_unpermute(const void *ys, const int32_t *rows, const float *w, const void *shared,
+                  const float *gate, int32_t T, int32_t H, int32_t n_rows, int32_t dtype, void *y,
+                  int32_t y_dtype, hipStream_t stream);
+
+/* Its gradients from dy [T][H] of `y_dtype`: dys[rows[8t + k]] = w[t][k] dy[t] (`dtype`),
+ * dw[t][k] = <dy[t], ys[rows[8t + k]]> (fp32; 0 for a dropped pair), and with a shared expert
+ * dshared[t] = gate[t] dy[t] (`dtype`) and dgate[t] = <dy[t], shared[t]> (fp32). shared, gate,
+ * dshared and dgate: all or none. */
+int moe_unpermute_backward(const void *dy, const void *ys, const int32_t *rows, const float *w,
+                           const void *shared, const float *gate, int32_t T, int32_t H,
+                           int32_t n_rows, int32_t dtype, int32_t y_dtype, void *dys, float *dw,
+                           void *dshared, float *dgate, hipStream_t stream);
+
+/* Rows as 8-bit integers with one fp32 scale each: scale[n] = max|x[n]| / 127 rounded to fp32 (1
+ * for a row of zeros; at least 2^-126), q[n][k] = the integer nearest to x[n][k] / scale[n] (the
+ * exact quotient, ties to even), so -127..127. A row that holds a NaN or an infinity gets the
+ * scale NaN and codes 0: its products are NaN. x [n][K] of `dtype`; n: 0..8388608; K: 16..16384, a
+ * multiple of 16. */
+int moe_quantize_i8(const void *x, int32_t n, int32_t K, int32_t dtype, int8_t *q, float *scale,
+                    hipStream_t stream);
+
+/* moe_permute of rows quantised as by moe_quantize_i8: xs [n_rows][H] codes and xs_scale [n_rows]
+ * in place of rows of `dtype`; H a multiple of 16. */
+int moe_permute_i8(const void *x, const int32_t *rows, int32_t T, int32_t H, int32_t n_rows,
+                   int32_t dtype, int8_t *xs, float *xs_scale, hipStream_t stream);
+
+/* Products of 8-bit integers, grouped by expert:
+ *   z[n][m] = x_scale[n] w_scale[e][m] sum_k x[n][k] w[e][m][k],  offsets[e] <= n < offsets[e + 1]
+ * x [n_rows][K] and w [E][M][K] int8 (16-byte aligned), x_scale [n_rows] and w_scale [E][M] fp32,
+ * offsets [E + 1] int32 in device memory as moe_bucket writes them, or NULL with E == 1 (all rows
+ * are the one matrix's). The sum is exact (32-bit integers); z = fp32(sum) * x_scale * w_scale in
+ * that order in fp32. swiglu == 0: y [n_rows][M] = z; otherwise M = 2I with the gate rows first and
+ * y [n_rows][I] = silu(z[n][i]) z[n][I + i]. y is rounded once to `y_dtype`. Rows outside
+ * [offsets[0], offsets[E]) are left as they were; offsets are clamped to [0, n_rows], and a row in two
+ * ranges gets either expert's result. n_rows: 0..8388608; E: 1..256; K: 16..16384, a multiple of 16; M: 8..65536, a multiple of 8 (of 16 with
+ * swiglu). */
+int moe_matmul_i8(const int8_t *x, const float *x_scale, int32_t n_rows, const int8_t *w,
+                  const float *w_scale, int32_t E, int32_t M, int32_t K, const int32_t *offsets,
+                  int32_t swiglu, void *y, int32_t y_dtype, hipStream_t stream);
 
 /* Static description of a status code. */
 const char *moe_status_str(int status);

@@ -27,8 +27,10 @@ WEIGHT_KEYS = ("router_w", "router_bias", "gate_up", "down", "shared_gate_up", "
                "gate_up_scale", "down_scale", "shared_gate_up_scale", "shared_down_scale")
 
 EXPORTS = ("moe_create", "moe_destroy", "moe_workspace_bytes", "moe_workspace_state_bytes",
-           "moe_route", "moe_bucket",
+           "moe_route", "moe_bucket", "moe_bucket_rows",
            "moe_forward", "moe_forward_noalloc", "moe_forward_plan", "moe_forward_timed",
+           "moe_permute", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
+           "moe_quantize_i8", "moe_permute_i8", "moe_matmul_i8",
            "moe_status_str")
 
 
@@ -69,6 +71,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_route.restype = ctypes.c_int
     lib.moe_bucket.argtypes = [P, P, I32, P, P, P, P, SZ, P]
     lib.moe_bucket.restype = ctypes.c_int
+    lib.moe_bucket_rows.argtypes = [P, P, I32, P, P, P, P, P, SZ, P]
+    lib.moe_bucket_rows.restype = ctypes.c_int
+    lib.moe_permute.argtypes = [P, P, I32, I32, I32, I32, P, P]
+    lib.moe_permute.restype = ctypes.c_int
+    lib.moe_permute_backward.argtypes = [P, P, I32, I32, I32, I32, P, P]
+    lib.moe_permute_backward.restype = ctypes.c_int
+    lib.moe_unpermute.argtypes = [P, P, P, P, P, I32, I32, I32, I32, P, I32, P]
+    lib.moe_unpermute.restype = ctypes.c_int
+    lib.moe_unpermute_backward.argtypes = [P, P, P, P, P, P, I32, I32, I32, I32, I32, P, P, P, P, P]
+    lib.moe_unpermute_backward.restype = ctypes.c_int
+    lib.moe_quantize_i8.argtypes = [P, I32, I32, I32, P, P, P]
+    lib.moe_quantize_i8.restype = ctypes.c_int
+    lib.moe_permute_i8.argtypes = [P, P, I32, I32, I32, I32, P, P, P]
+    lib.moe_permute_i8.restype = ctypes.c_int
+    lib.moe_matmul_i8.argtypes = [P, P, I32, P, P, I32, I32, I32, P, I32, P, I32, P]
+    lib.moe_matmul_i8.restype = ctypes.c_int
     lib.moe_forward.argtypes = [P, P, I32, P, P, P, P, P, SZ, P]
     lib.moe_forward.restype = ctypes.c_int
     lib.moe_forward_noalloc.argtypes = [P, P, I32, P, P, P, P, P]
@@ -191,6 +209,25 @@ class MoeLayer:
                "moe_bucket")
         return counts, offsets, perm
 
+    def bucket_rows(self, ids, ws=None, stream=None):
+        """(counts [E], offsets [E+1], perm [T*8], rows [T*8]): bucket() and the inverse of perm,
+        the table that the row operators below take (-1: the pair's id is outside [0, E))."""
+        import torch
+        T = ids.shape[0]
+        dev = ids.device
+        counts = torch.empty((self.num_experts,), dtype=torch.int32, device=dev)
+        offsets = torch.empty((self.num_experts + 1,), dtype=torch.int32, device=dev)
+        perm = torch.empty((T * 8,), dtype=torch.int32, device=dev)
+        rows = torch.empty((T * 8,), dtype=torch.int32, device=dev)
+        if T == 0:  # the library enqueues nothing: no pairs
+            counts.zero_()
+            offsets.zero_()
+        ws = self.workspace(T, dev) if ws is None else ws
+        _check(self.lib.moe_bucket_rows(self.ctx, _ptr(ids), T, _ptr(counts), _ptr(offsets),
+                                        _ptr(perm), _ptr(rows), _ptr(ws), ws.numel(),
+                                        _stream(stream)), "moe_bucket_rows")
+        return counts, offsets, perm, rows
+
     def forward(self, x, routing=None, y=None, ws=None, stream=None, events=None):
         """y [T][H] fp32; routing = (ids, w, g) to use a given routing, else routed from x."""
         import torch
@@ -231,6 +268,216 @@ class MoeLayer:
         _check(self.lib.moe_forward_plan(self.ctx, T, int(routing_given), ctypes.byref(n), names,
                                          16), "moe_forward_plan")
         return [names[i].decode() for i in range(n.value)]
+
+
+# ---------------------------------------------------------------- separate operators
+# Rows sorted by expert and back, their gradients, and products of 8-bit integers, around a
+# caller's own expert products. rows is the [T*8] int32 table of MoeLayer.bucket_rows. Tensors are
+# contiguous and on one device; what is not raises ValueError before anything is enqueued, and so
+# does a call that the library refuses (MoeError). Without `stream` the work is enqueued on the
+# tensors' device's current stream; with it, results are allocated for that stream, and the
+# caller orders it after whatever writes the inputs.
+
+def _want(name, t, dtype, shape, device):
+    """t as a contiguous tensor of the dtype (or one of them), shape (None: any) and device."""
+    if not (t.dtype in dtype if isinstance(dtype, tuple) else t.dtype is dtype):
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+def _row_types():
+    import torch
+    return torch.float32, torch.bfloat16
+
+
+def _enum(dtype):
+    import torch
+    if dtype is torch.bfloat16:
+        return MOE_BF16
+    if dtype is torch.float32:
+        return MOE_F32
+    raise ValueError(f"dtype {dtype}: torch.float32 or torch.bfloat16")
+
+
+class _On:
+    """Context of one call: the tensors' device current, and the given stream current on it, so
+    that what the call allocates belongs to the stream that writes it."""
+
+    def __init__(self, device, stream):
+        import torch
+        if device.type != "cuda":
+            raise ValueError(f"tensors must be on a GPU, not on {device}")
+        self.ctx = None
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"stream of {stream.device}, tensors on {device}")
+            self.ctx = torch.cuda.stream(stream)
+        elif device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(device)
+
+    def __enter__(self):
+        import torch
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            return self.ctx.__exit__(*exc)
+        return None
+
+
+def permute(x, rows, n_rows=None, xs=None, stream=None):
+    """xs [n_rows][H] with xs[rows[8t + k]] = x[t] for x [T][H] (fp32 or bf16); n_rows: by default
+    T * 8, or the rows of xs. Rows that no pair names keep what xs held."""
+    import torch
+    T, H = x.shape
+    dev = x.device
+    px, pr = _want("x", x, _row_types(), (T, H), dev), _want("rows", rows, torch.int32, (T * 8,), dev)
+    with _On(dev, stream) as s:
+        if xs is None:
+            xs = torch.empty((T * 8 if n_rows is None else n_rows, H), dtype=x.dtype, device=dev)
+        n = xs.shape[0] if n_rows is None else n_rows
+        _check(load().moe_permute(px, pr, T, H, n, _enum(x.dtype),
+                                  _want("xs", xs, x.dtype, (n, H), dev), s), "moe_permute")
+    return xs
+
+
+def permute_backward(dxs, rows, dx=None, stream=None):
+    """dx [T][H] with dx[t] = sum_k dxs[rows[8t + k]]: the gradient of permute."""
+    import torch
+    n, H = dxs.shape
+    dev = dxs.device
+    T = rows.numel() // 8
+    pd = _want("dxs", dxs, _row_types(), (n, H), dev)
+    pr = _want("rows", rows, torch.int32, (T * 8,), dev)
+    with _On(dev, stream) as s:
+        if dx is None:
+            dx = torch.empty((T, H), dtype=dxs.dtype, device=dev)
+        _check(load().moe_permute_backward(pd, pr, T, H, n, _enum(dxs.dtype),
+                                           _want("dx", dx, dxs.dtype, (T, H), dev), s),
+               "moe_permute_backward")
+    return dx
+
+
+def unpermute(ys, rows, w, shared=None, gate=None, dtype=None, y=None, stream=None):
+    """y [T][H] with y[t] = sum_k w[t][k] ys[rows[8t + k]] + gate[t] shared[t]; y of `dtype`
+    (by default that of ys)."""
+    import torch
+    n, H = ys.shape
+    dev = ys.device
+    T = w.shape[0]
+    f32 = torch.float32
+    py = _want("ys", ys, _row_types(), (n, H), dev)
+    pr = _want("rows", rows, torch.int32, (T * 8,), dev)
+    pw = _want("w", w, f32, (T, 8), dev)
+    if (shared is None) != (gate is None):
+        raise ValueError("shared and gate: both or neither")
+    ps = None if shared is None else _want("shared", shared, ys.dtype, (T, H), dev)
+    pg = None if gate is None else _want("gate", gate, f32, (T,), dev)
+    with _On(dev, stream) as s:
+        if y is None:
+            y = torch.empty((T, H), dtype=ys.dtype if dtype is None else dtype, device=dev)
+        elif dtype is not None and y.dtype != dtype:
+            raise ValueError(f"y: dtype {y.dtype}, expected {dtype}")
+        _check(load().moe_unpermute(py, pr, pw, ps, pg, T, H, n, _enum(ys.dtype),
+                                    _want("y", y, _row_types(), (T, H), dev), _enum(y.dtype), s),
+               "moe_unpermute")
+    return y
+
+
+def unpermute_backward(dy, ys, rows, w, shared=None, gate=None, dys=None, stream=None):
+    """(dys [n][H], dw [T][8], dshared [T][H] or None, dgate [T] or None): the gradients of
+    unpermute. Rows of dys that no pair names keep what it held."""
+    import torch
+    n, H = ys.shape
+    dev = ys.device
+    T = w.shape[0]
+    f32 = torch.float32
+    pd = _want("dy", dy, _row_types(), (T, H), dev)
+    py = _want("ys", ys, _row_types(), (n, H), dev)
+    pr = _want("rows", rows, torch.int32, (T * 8,), dev)
+    pw = _want("w", w, f32, (T, 8), dev)
+    if (shared is None) != (gate is None):
+        raise ValueError("shared and gate: both or neither")
+    ps = None if shared is None else _want("shared", shared, ys.dtype, (T, H), dev)
+    pg = None if gate is None else _want("gate", gate, f32, (T,), dev)
+    with _On(dev, stream) as s:
+        if dys is None:
+            dys = torch.empty((n, H), dtype=ys.dtype, device=dev)
+        dw = torch.empty((T, 8), dtype=f32, device=dev)
+        dshared = None if shared is None else torch.empty_like(shared)
+        dgate = None if shared is None else torch.empty_like(gate)
+        _check(load().moe_unpermute_backward(
+            pd, py, pr, pw, ps, pg, T, H, n, _enum(ys.dtype), _enum(dy.dtype),
+            _want("dys", dys, ys.dtype, (n, H), dev), dw.data_ptr(),
+            None if shared is None else dshared.data_ptr(),
+            None if shared is None else dgate.data_ptr(), s), "moe_unpermute_backward")
+    return dys, dw, dshared, dgate
+
+
+def quantize_i8(x, stream=None):
+    """(codes [n][K] int8, scales [n] fp32) of the rows of x [n][K] (fp32 or bf16)."""
+    import torch
+    n, K = x.shape
+    dev = x.device
+    px = _want("x", x, _row_types(), (n, K), dev)
+    with _On(dev, stream) as s:
+        q = torch.empty((n, K), dtype=torch.int8, device=dev)
+        scale = torch.empty((n,), dtype=torch.float32, device=dev)
+        _check(load().moe_quantize_i8(px, n, K, _enum(x.dtype), q.data_ptr(), scale.data_ptr(), s),
+               "moe_quantize_i8")
+    return q, scale
+
+
+def permute_i8(x, rows, n_rows=None, stream=None):
+    """(codes [n_rows][H] int8, scales [n_rows] fp32): the rows of x [T][H] quantised and sorted,
+    as permute(x, rows) followed by quantize_i8. n_rows: by default T * 8. Rows that no pair names
+    are not written."""
+    import torch
+    T, H = x.shape
+    dev = x.device
+    n = T * 8 if n_rows is None else n_rows
+    px, pr = _want("x", x, _row_types(), (T, H), dev), _want("rows", rows, torch.int32, (T * 8,), dev)
+    with _On(dev, stream) as s:
+        q = torch.empty((n, H), dtype=torch.int8, device=dev)
+        scale = torch.empty((n,), dtype=torch.float32, device=dev)
+        _check(load().moe_permute_i8(px, pr, T, H, n, _enum(x.dtype), q.data_ptr(),
+                                     scale.data_ptr(), s), "moe_permute_i8")
+    return q, scale
+
+
+def matmul_i8(x, x_scale, w, w_scale, offsets=None, swiglu=False, dtype=None, y=None, stream=None):
+    """y [n][M] = x_scale[n] w_scale[e][m] sum_k x[n][k] w[e][m][k] for int8 x [n][K] and
+    w [E][M][K], e the expert with offsets[e] <= n < offsets[e + 1] (offsets [E + 1] int32 on the
+    device; None: w holds one matrix for all rows). swiglu: w holds gate rows, then up rows, and
+    y [n][M / 2] = silu(gate) up. y of `dtype`, bf16 by default; rows of no expert keep what it
+    held."""
+    import torch
+    n, K = x.shape
+    E, M = w.shape[0], w.shape[1]
+    dev = x.device
+    f32 = torch.float32
+    px, ps = _want("x", x, torch.int8, (n, K), dev), _want("x_scale", x_scale, f32, (n,), dev)
+    pw = _want("w", w, torch.int8, (E, M, K), dev)
+    pc = _want("w_scale", w_scale, f32, (E, M), dev)
+    po = None if offsets is None else _want("offsets", offsets, torch.int32, (E + 1,), dev)
+    Mo = M // 2 if swiglu else M
+    with _On(dev, stream) as s:
+        if y is None:
+            y = torch.empty((n, Mo), dtype=torch.bfloat16 if dtype is None else dtype, device=dev)
+        elif dtype is not None and y.dtype != dtype:
+            raise ValueError(f"y: dtype {y.dtype}, expected {dtype}")
+        _check(load().moe_matmul_i8(px, ps, n, pw, pc, E, M, K, po, int(bool(swiglu)),
+                                    _want("y", y, _row_types(), (n, Mo), dev), _enum(y.dtype), s),
+               "moe_matmul_i8")
+    return y
 
 
 def device_weights(layer: dict, device="cuda") -> dict:

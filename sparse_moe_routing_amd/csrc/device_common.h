@@ -36,6 +36,13 @@ __device__ __forceinline__ uint32_t f32_to_bf16_bits(float f) {
     return (b + 0x7FFFu + ((b >> 16) & 1u)) >> 16;
 }
 
+// Two fp32 rounded to bf16 (nearest-even; infinities and NaN kept), the first in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    typedef __bf16 pair_t __attribute__((ext_vector_type(2)));
+    const pair_t v = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
 struct OpBF16 {
     using elem_t = uint16_t;
     static constexpr int kElemBytes = 2;
@@ -218,6 +225,19 @@ __device__ __forceinline__ void scale_rows(f32x4_t &acc, const float *scale) {
 }
 
 __device__ __forceinline__ int lane_id() { return threadIdx.x & (kWave - 1); }
+
+// Inclusive prefix sum over the 64 lanes of a wave with DPP lane moves (no LDS round trips):
+// shifts by 1, 2, 4, 8 inside each 16-lane row, then each row adds the total of the row before
+// (broadcasts of lanes 15 and 31).
+__device__ __forceinline__ int wave_inclusive_sum(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);  // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);  // row_shr:2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);  // row_shr:4
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);  // row_shr:8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false); // row_bcast:15 to rows 1, 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false); // row_bcast:31 to rows 2, 3
+    return v;
+}
 
 // Device-coherent access for data that one wave writes and a wave on another XCD reads inside the
 // same launch: relaxed agent-scope atomic loads and stores (on gfx950 these carry the device

@@ -51,6 +51,7 @@ struct BucketParams {
     int32_t *counts;     // [E]
     int32_t *offsets;    // [E+1]
     int32_t *perm;       // [T*8]
+    int32_t *rows;       // [T*8] the inverse of perm (-1: dropped), or nullptr
     int32_t *hist;       // the chunks' expert histograms (multi-block path), then per-chunk
                          // bases: [n_chunks][E], or [E][n_chunks] above kScanOneBlockChunks
                          // chunks (hist_at)
@@ -133,6 +134,50 @@ struct CombineParams {
     float *y;            // [T][H]
     int T, H, E, slots, n_sc_routed, n_sc_shared, has_shared;
 };
+
+// Separate operators (permute.hip, int8.hip): rows [T][8] is the pairs' row in the sorted buffers.
+struct UnpermuteParams {
+    const void *ys;      // [n_rows][H]
+    const int32_t *rows;
+    const float *w;      // [T][8]; nullptr: a plain sum (the gradient of the sort)
+    const void *shared;  // [T][H] or nullptr
+    const float *gate;   // [T] or nullptr
+    void *y;             // [T][H]
+    int T, H, n_rows;
+};
+
+struct UnpermuteBwdParams {
+    const void *dy, *ys;
+    const int32_t *rows;
+    const float *w;
+    const void *shared;
+    const float *gate;
+    void *dys;
+    float *dw;
+    void *dshared;
+    float *dgate;
+    int T, H, n_rows;
+};
+
+struct I8Params {
+    const int8_t *x;         // [n_rows][K]
+    const float *x_scale;    // [n_rows]
+    const int8_t *w;         // [E][M][K]
+    const float *w_scale;    // [E][M]
+    const int32_t *offsets;  // [E + 1], or nullptr: every row is expert 0's
+    void *y;                 // [n_rows][M], with SwiGLU [n_rows][M / 2]
+    int n_rows, E, M, K;
+};
+
+// Element types: 0 fp32, 1 bf16.
+hipError_t launch_permute(const void *x, const int32_t *rows, int T, int H, int n_rows, int dtype,
+                          void *xs, hipStream_t s);
+hipError_t launch_unpermute(const UnpermuteParams &p, int dtype, int y_dtype, hipStream_t s);
+hipError_t launch_unpermute_backward(const UnpermuteBwdParams &p, int dtype, int y_dtype,
+                                     hipStream_t s);
+hipError_t launch_quantize_i8(const void *x, const int32_t *rows, int n, int K, int n_rows,
+                              int dtype, int8_t *q, float *scale, hipStream_t s);
+hipError_t launch_matmul_i8(const I8Params &p, bool swiglu, int y_dtype, hipStream_t s);
 
 hipError_t launch_router(const RouterParams &p, int dtype, int maxrt, hipStream_t s);
 hipError_t launch_route_small(const SelectParams &sp, const BucketParams &bp, bool do_select,

@@ -710,6 +710,24 @@ int forward_impl(const moe_ctx *c, const void *x, int32_t T, const int32_t *ids_
     return hip_status(L.err);
 }
 
+int bucket_impl(const moe_ctx *c, const int32_t *ids_in, int32_t T, int32_t *counts,
+                int32_t *offsets, int32_t *perm, int32_t *rows, void *workspace, size_t ws_bytes,
+                hipStream_t stream) {
+    if (!c) return MOE_ERR_INVALID_ARG;
+    if (T < 0 || T > c->cfg.max_tokens) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!ids_in || !counts || !offsets || !perm) return MOE_ERR_INVALID_ARG;
+    const Plan p = make_plan(c, T);
+    const int st = check_call(c, T, workspace, ws_bytes, &p);
+    if (st != MOE_OK) return st;
+    Launcher L{c, stream, nullptr, 0, true};
+    char *ws = static_cast<char *>(workspace);
+    BucketParams bp = bucket_params(c, p, ws, ids_in, counts, offsets, perm);
+    bp.rows = rows;
+    enqueue_dispatch(L, p, nullptr, bp, ws);
+    return hip_status(L.err);
+}
+
 bool valid_inter(int v, int dtype) {
     // FP8 weights run only the chunked expert kernels: 128-element weight-row chunks; MXFP4
     // weights stream chunk pairs (256 weights, 128 bytes of codes per row)
@@ -945,17 +963,14 @@ int moe_route(const moe_ctx *c, const void *x, const float *logits_in, int32_t T
 int moe_bucket(const moe_ctx *c, const int32_t *ids_in, int32_t T, int32_t *counts,
                int32_t *offsets, int32_t *perm, void *workspace, size_t ws_bytes,
                hipStream_t stream) {
-    if (!c) return MOE_ERR_INVALID_ARG;
-    if (T < 0 || T > c->cfg.max_tokens) return MOE_ERR_INVALID_ARG;
-    if (T == 0) return MOE_OK;
-    if (!ids_in || !counts || !offsets || !perm) return MOE_ERR_INVALID_ARG;
-    const Plan p = make_plan(c, T);
-    const int st = check_call(c, T, workspace, ws_bytes, &p);
-    if (st != MOE_OK) return st;
-    Launcher L{c, stream, nullptr, 0, true};
-    char *ws = static_cast<char *>(workspace);
-    enqueue_dispatch(L, p, nullptr, bucket_params(c, p, ws, ids_in, counts, offsets, perm), ws);
-    return hip_status(L.err);
+    return bucket_impl(c, ids_in, T, counts, offsets, perm, nullptr, workspace, ws_bytes, stream);
+}
+
+int moe_bucket_rows(const moe_ctx *c, const int32_t *ids_in, int32_t T, int32_t *counts,
+                    int32_t *offsets, int32_t *perm, int32_t *rows, void *workspace,
+                    size_t ws_bytes, hipStream_t stream) {
+    if (c && T > 0 && T <= c->cfg.max_tokens && !rows) return MOE_ERR_INVALID_ARG;
+    return bucket_impl(c, ids_in, T, counts, offsets, perm, rows, workspace, ws_bytes, stream);
 }
 
 int moe_forward(const moe_ctx *c, const void *x, int32_t T, const int32_t *ids_in,

@@ -92,10 +92,12 @@ __device__ int chunk_counts(S &s, int n, int E) {
 }
 
 // Writes perm[base_of(e) + stable rank] = p0 + pair index for every valid pair (sub-chunks as
-// in chunk_counts). base_of(e) gives the destination of expert e's first pair of this chunk.
-// Needs s.pre, i.e. a block barrier after chunk_counts.
+// in chunk_counts) and, where rows is given, the inverse: rows[p0 + pair index] = that position,
+// -1 for a pair without a valid id. base_of(e) gives the destination of expert e's first pair of
+// this chunk. Needs s.pre, i.e. a block barrier after chunk_counts.
 template <class S, class Base>
-__device__ void chunk_scatter(const S &s, int n, int E, int p0, int32_t *perm, Base base_of) {
+__device__ void chunk_scatter(const S &s, int n, int E, int p0, int32_t *perm, int32_t *rows,
+                              Base base_of) {
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int nw = blockDim.x / kWave;
@@ -106,22 +108,13 @@ __device__ void chunk_scatter(const S &s, int n, int E, int p0, int32_t *perm, B
         if (e >= 0 && e < E) {
             const uint64_t m = lanes_of(s, sc, e);
             const int rank = __popcll(m & ((1ull << lane) - 1ull));
-            perm[base_of(e) + s.pre[sc][e] + rank] = p0 + pidx;
+            const int at = base_of(e) + s.pre[sc][e] + rank;
+            perm[at] = p0 + pidx;
+            if (rows) rows[p0 + pidx] = at;
+        } else if (rows && pidx < n) {
+            rows[p0 + pidx] = -1;
         }
     }
-}
-
-// Inclusive prefix sum over the 64 lanes of a wave with DPP lane moves (no LDS round trips):
-// shifts by 1, 2, 4, 8 inside each 16-lane row, then each row adds the total of the row before
-// (broadcasts of lanes 15 and 31).
-__device__ __forceinline__ int wave_inclusive_sum(int v) {
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);  // row_shr:1
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);  // row_shr:2
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);  // row_shr:4
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);  // row_shr:8
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false); // row_bcast:15 to rows 1, 3
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false); // row_bcast:31 to rows 2, 3
-    return v;
 }
 
 // Exclusive scans over experts of s.a and s.b (256 entries each, by wave 0 of the block).
@@ -271,11 +264,14 @@ __device__ void bucket_wave(const BucketParams &bp, int n, int lane, S &s) {
     if (ok) {
         const int off = s.a[e];
         bp.perm[off + rank] = lane;
+        if (bp.rows) bp.rows[lane] = off + rank;
         if (first) {
             const int gb = nsh + s.b[e];
             for (int gg = 0; gg < ngrp; ++gg)
                 bp.groups[gb + gg] = make_int4(e, off + gg * bp.NG, min(bp.NG, cnt - gg * bp.NG), 0);
         }
+    } else if (bp.rows && lane < n) {
+        bp.rows[lane] = -1;
     }
     if (lane < nsh) bp.groups[lane] = make_int4(bp.E, lane * bp.NG, min(bp.NG, bp.T - lane * bp.NG), 0);
     const int ctot = __builtin_amdgcn_readlane(ci, kWave - 1), gtot = __builtin_amdgcn_readlane(gi, kWave - 1);
@@ -315,7 +311,7 @@ __device__ void select_bucket_block(const SelectParams &sp, const BucketParams &
     }
     const int cnt = chunk_counts(s, n, bp.E);
     write_tables(bp, cnt, s);  // ends with a barrier; s.a[e] = offset of expert e
-    chunk_scatter(s, n, bp.E, 0, bp.perm, [&](int e) { return s.a[e]; });
+    chunk_scatter(s, n, bp.E, 0, bp.perm, bp.rows, [&](int e) { return s.a[e]; });
 }
 
 // T <= 64 with given ids (or selection from given logits): one block.
@@ -395,7 +391,7 @@ __global__ __launch_bounds__(1024) void route_tiles_kernel(RouterParams rp, Sele
     __syncthreads();
     const int cnt = chunk_counts(s, n, bp.E);
     write_tables(bp, cnt, s);  // ends with a barrier; s.a[e] = offset of expert e
-    chunk_scatter(s, n, bp.E, 0, bp.perm, [&](int e) { return s.a[e]; });
+    chunk_scatter(s, n, bp.E, 0, bp.perm, bp.rows, [&](int e) { return s.a[e]; });
 }
 
 // T > 64, pass 1: per chunk of chunk_tokens tokens (one wave each), selection (optional) and
@@ -462,7 +458,7 @@ __global__ __launch_bounds__(1024) void select_bucket_kernel(SelectParams sp, Bu
     __syncthreads();
     const int cnt = chunk_counts(s, n, bp.E);
     write_tables(bp, cnt, s);  // ends with a barrier; s.a[e] = offset of expert e
-    chunk_scatter(s, n, bp.E, 0, bp.perm, [&](int e) { return s.a[e]; });
+    chunk_scatter(s, n, bp.E, 0, bp.perm, bp.rows, [&](int e) { return s.a[e]; });
 }
 
 // T > 256, pass 2 with up to kScanOneBlockChunks chunks (one block): per-expert running bases
@@ -574,7 +570,7 @@ __global__ __launch_bounds__(512) void bucket_scatter_kernel(BucketParams bp) {
     __syncthreads();
     chunk_counts(s, nt * kTopK, bp.E);
     __syncthreads();
-    chunk_scatter(s, nt * kTopK, bp.E, t0 * kTopK, bp.perm,
+    chunk_scatter(s, nt * kTopK, bp.E, t0 * kTopK, bp.perm, bp.rows,
                   [&](int e) { return bp.offsets[e] + bp.hist[hist_at(bp, blockIdx.x, e)]; });
 }
 
