@@ -5,6 +5,10 @@
 // and is exact in any order, so every variant and split gives the same bits; only the two scales
 // and the SwiGLU are fp32 arithmetic. Weights are the A operand and rows the B operand: a lane's
 // accumulators are four consecutive channels of one row, stored as one piece.
+#include <math.h>
+
+#include <atomic>
+
 #include "device_common.h"
 #include "kernels.h"
 
@@ -19,8 +23,9 @@ __device__ __forceinline__ void mma_i8(i32x4_t &acc, const uint4 &a, const uint4
                                                 __builtin_bit_cast(i32x4_t, b), acc, 0, 0, 0);
 }
 
-// Row tiles of the experts in order: expert e's rows [lo, hi) in tiles of `per` rows. Every wave
-// finds tile u by itself: lane l sums the tiles of experts 4l .. 4l + 3, a wave scan places them.
+// Row tiles of the experts in order: expert e's rows [lo, hi) in as few tiles of at most `per` rows
+// as hold them, of even sizes (multiples of 16 but for the last). Every wave finds tile u by itself:
+// lane l sums the tiles of experts 4l .. 4l + 3, a wave scan places them.
 struct RowTile {
     int e, start, n;  // n = 0: there is no such tile
 };
@@ -45,16 +50,17 @@ __device__ __forceinline__ TileScan scan_tiles(const int32_t *offsets, int E, in
     s.total = __builtin_amdgcn_readlane(incl, kWave - 1);
     return s;
 }
-__device__ __forceinline__ RowTile pick_tile(const TileScan &s, int per, int u) {
+__device__ __forceinline__ RowTile pick_tile(const TileScan &s, int lane, int u) {
     int at = s.at, e = 0, start = 0, n = 0;
     bool mine = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (u >= at && u < at + s.nt[i]) {
             mine = true;
-            e = 4 * lane_id() + i;
-            start = s.lo[i] + (u - at) * per;
-            n = min(per, s.hi[i] - start);
+            e = 4 * lane + i;
+            const int rows = s.hi[i] - s.lo[i], part = ((rows + s.nt[i] - 1) / s.nt[i] + 15) & ~15;
+            start = s.lo[i] + (u - at) * part;
+            n = min(part, s.hi[i] - start);
         }
         at += s.nt[i];
     }
@@ -72,76 +78,37 @@ __device__ __forceinline__ void store4(uint16_t *p, const float (&v)[4]) {
     *reinterpret_cast<uint2 *>(p) = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
 }
 
+// silu(z) = z / (1 + e^-z) in about ten instructions (the epilogue of a gate/up product forms one
+// for every two sums): e^-z = 2^t (1 + c), t the rounded product -z log2(e) and c the part that
+// the rounding and the constant left off, so that the error stays a few steps of fp32 however
+// large z is. The bound on the exponent keeps t and c finite; past it e^-z is 0 or infinite anyway.
+__device__ __forceinline__ float silu(float z) {
+    constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596299e-8f, kLn2 = 0.693147182f;
+    const float a = __builtin_amdgcn_fmed3f(-z, -150.0f, 150.0f);
+    const float t = a * kLog2e;
+    const float c = fmaf(a, kLog2eRest, fmaf(a, kLog2e, -t)) * kLn2;
+    const float e = __builtin_amdgcn_exp2f(t) * (1.0f + c);
+    return z * __builtin_amdgcn_rcpf(1.0f + e);
+}
+
 // z = fp32(sum) * x_scale * w_scale of four channels.
 __device__ __forceinline__ void scaled(const i32x4_t &acc, float sx, const float *sw, float (&z)[4]) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) z[r] = (float)acc[r] * sx * sw[r];
 }
 
-// Tiles of 64 rows by 64 output channels, 16 channels per wave (with SwiGLU: 16 gate and the 16
-// matching up channels).
-constexpr int kTRows = 64, kTCols = 64;
-template <bool kSwiglu, class O>
-__global__ __launch_bounds__(256) void i8_tile_kernel(I8Params p) {
-    constexpr int kA = kSwiglu ? 2 : 1;
-    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int col = lane & 15, q = lane >> 4;
-    const int Mo = kSwiglu ? p.M / 2 : p.M;
-    const int cb = (Mo + kTCols - 1) / kTCols;
-    const int u = blockIdx.x / cb, m0 = (blockIdx.x % cb) * kTCols + wave * kTile;
-    const RowTile t = p.offsets ? pick_tile(scan_tiles(p.offsets, p.E, p.n_rows, kTRows), kTRows, u)
-                                : RowTile{0, u * kTRows, min(kTRows, p.n_rows - u * kTRows)};
-    if (t.n <= 0 || m0 >= Mo) return;
-    const int mrow = min(m0 + col, Mo - 1);
-    const int8_t *w[kA];
-#pragma unroll
-    for (int a = 0; a < kA; ++a) w[a] = p.w + ((size_t)t.e * p.M + a * Mo + mrow) * p.K;
-    const int8_t *x[kTRows / kTile];
-#pragma unroll
-    for (int i = 0; i < kTRows / kTile; ++i)
-        x[i] = p.x + (size_t)(t.start + min(i * kTile + col, t.n - 1)) * p.K;
-    i32x4_t acc[kA][kTRows / kTile] = {};
-    for (int k = q * 16; k < (p.K + 63) / 64 * 64; k += 64) {
-        const bool in = k < p.K;
-        const uint4 z = {0, 0, 0, 0};
-        uint4 a[kA];
-#pragma unroll
-        for (int i = 0; i < kA; ++i) a[i] = in ? load16(w[i] + k) : z;
-#pragma unroll
-        for (int j = 0; j < kTRows / kTile; ++j) {
-            const uint4 b = in ? load16(x[j] + k) : z;
-#pragma unroll
-            for (int i = 0; i < kA; ++i) mma_i8(acc[i][j], a[i], b);
-        }
-    }
-    const int mc = m0 + 4 * q;
-    if (mc >= Mo) return;  // Mo is a multiple of 8: a lane's four channels are all in or all out
-    const float *sw = p.w_scale + (size_t)t.e * p.M + mc;
-#pragma unroll
-    for (int j = 0; j < kTRows / kTile; ++j) {
-        const int n = j * kTile + col;
-        if (n >= t.n) continue;
-        const float sx = p.x_scale[t.start + n];
-        float z[4];
-        scaled(acc[0][j], sx, sw, z);
-        if constexpr (kSwiglu) {
-            float up[4];
-            scaled(acc[1][j], sx, sw + Mo, up);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) z[r] = z[r] / (1.0f + expf(-z[r])) * up[r];
-        }
-        store4(reinterpret_cast<O *>(p.y) + (size_t)(t.start + n) * Mo + mc, z);
-    }
-}
-
 // ------------------------------------------------------------------------- large row counts
 // A block multiplies up to 320 rows of one expert by 256 weight channels (with SwiGLU: 128 gate
 // channels and the 128 up channels that go with them). K is staged in slabs of 128 bytes per row,
-// loaded straight into LDS (buffer loads with the LDS flag: no registers held while in flight),
-// double-buffered: the next slab's loads are in flight during the current slab's matrix
-// instructions, one block barrier per slab. Eight waves, two per SIMD: wave w takes the channels
-// of half w % 2 and a quarter of the tile's 16-row subtiles, at most five, so that a tile of n rows
-// costs ceil(n / 64) subtiles of matrix work per wave whatever n is.
+// whole cache lines loaded straight into LDS (buffer loads with the LDS flag: no registers held
+// while in flight), double-buffered: the next slab's loads are in flight during the current slab's
+// matrix instructions, one block barrier per slab. Eight waves, two per SIMD: wave w takes the
+// channels of half w % 2 and a quarter of the tile's 16-row subtiles, at most five, so that a tile
+// of n rows costs ceil(n / 64) subtiles of matrix work per wave whatever n is.
+//
+// A block's 144 KB of slabs leave one block per CU, so nothing else would cover a unit's start and
+// end: the blocks are persistent, one per CU, and the last slab of a unit is multiplied (and its
+// results are scaled and stored) while the first slab and the scales of the block's next unit load.
 //
 // Bounds come from the buffer resources: the row resource covers exactly the tile's n rows and the
 // weight resource the expert's remaining channels, so that loads past either return zeros without
@@ -154,6 +121,7 @@ constexpr int kXSegs = kBRows * kSlabB / 1024 / kBWaves;  // 1 KB row segments p
 constexpr int kWSegs = kBCh * kSlabB / 1024 / kBWaves;    // 1 KB weight segments per wave (4)
 constexpr int kXcds = 8;
 constexpr uint32_t kPast = 0xFFFFFFF0u;   // a buffer offset past every range
+constexpr uint32_t kFar = 0x80000000u;    // the same with any row's offset added (they stay below 2^30)
 
 // Position of 16-byte piece pc (0..7) of staged row r: rows 2m and 2m + 1 rotate by m, so the 16
 // rows of one operand read lie on distinct bank groups; rows 16 apart keep their pieces' order.
@@ -163,177 +131,531 @@ __device__ __forceinline__ int spos(int r, int pc) { return r * kSlabB + ((pc ^ 
 // reads of the other.
 __shared__ __align__(16) unsigned char b_w0[kBCh * kSlabB], b_w1[kBCh * kSlabB];
 __shared__ __align__(16) unsigned char b_x0[kBRows * kSlabB], b_x1[kBRows * kSlabB];
+// Scales of the current and the next unit: rows, then staged weight rows.
+__shared__ __align__(16) float b_scale[2][kBRows + kBCh];
 
-__device__ __forceinline__ void to_lds16(__amdgpu_buffer_rsrc_t r, unsigned char *seg, uint32_t off) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)seg, 16,
-                                             (int)off, 0, 0, 0);
+template <int kAux>
+__device__ __forceinline__ void to_lds16(__amdgpu_buffer_rsrc_t r, void *seg, uint32_t off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)seg, 16, (int)off,
+                                             0, 0, kAux);
+}
+__device__ __forceinline__ void to_lds4(__amdgpu_buffer_rsrc_t r, void *seg, uint32_t off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)seg, 4, (int)off,
+                                             0, 0, 0);
 }
 
-template <bool kSwiglu, class O, int kN>
-__device__ __forceinline__ void block_product(const I8Params &p, const RowTile &t, int m0) {
-    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// The scan of the row tiles, kept out of the registers of the products (written by wave 0).
+__shared__ TileScan b_scan[kWave];
+
+// Lanes of a wave exchange values through LDS: fenced at wavefront scope, without which the
+// compiler may forward a lane's own earlier store to its load.
+__device__ __forceinline__ void wave_exchange() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// One unit: a row tile and its first output channel.
+struct Unit {
+    RowTile t;
+    int m0;
+};
+
+template <bool kSwiglu, class O, bool kOnce>
+struct BlockProduct {
+    static constexpr int kCols = kSwiglu ? kBCh / 2 : kBCh;  // output channels of a block
+    static constexpr int kAux = kOnce ? kBufNT : 0;          // cache policy of the weights
+    const I8Params &p;
+    int lane, wave, ch, th, Mo;
+    int nslab;
+
+    __device__ __forceinline__ BlockProduct(const I8Params &p_) : p(p_) {
+        lane = lane_id();
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        ch = wave & 1;
+        th = (wave >> 1) & 3;
+        Mo = kSwiglu ? p.M / 2 : p.M;
+        nslab = (p.K + kSlabB - 1) / kSlabB;
+    }
+    // The lane number, made anew: what is computed from it stays next to its use instead of in
+    // registers across the products, which need them all.
+    __device__ __forceinline__ int here() const {
+        int l = lane;
+        asm volatile("" : "+v"(l));
+        return l;
+    }
+    // weight channel (past m0) of staged row R; SwiGLU: each half of 128 staged rows holds 64 gate
+    // channels, then the 64 matching up channels
+    __device__ __forceinline__ int channel(int R) const {
+        return kSwiglu ? (R >> 7) * 64 + (R & 63) + ((R >> 6) & 1) * Mo : R;
+    }
+    // Slab s of an operand: segment g holds rows 8g .. 8g + 7; lane l of its load writes position
+    // l % 8 of row l / 8, so it reads the piece that the row's rotation puts there. row(g): the
+    // segment's first row in memory, negative when the whole segment is past the operand (it is
+    // not loaded: its results are dropped). Pieces at or past K read as zero.
+    template <int kSegs, int kAuxBits, class Row>
+    __device__ __forceinline__ void issue(__amdgpu_buffer_rsrc_t r, unsigned char *buf, int s, Row row) const {
+        const int l = here(), pc = ((l & 7) ^ (l >> 4)) * 16, left = p.K - s * kSlabB;
+        const uint32_t at = (uint32_t)(l >> 3) * p.K;
+        const uint32_t even = pc < left ? at + pc : kFar, odd = (pc ^ 64) < left ? at + (pc ^ 64) : kFar;
+#pragma unroll
+        for (int a = 0; a < kSegs; ++a) {
+            const int g = kSegs * wave + a, first = row(g);
+            if (first >= 0)  // uniform
+                to_lds16<kAuxBits>(r, buf + g * 1024, (g & 1 ? odd : even) + (uint32_t)(first * p.K + s * kSlabB));
+        }
+    }
+    __device__ __forceinline__ void issue_x(const Unit &u, unsigned char *xb, int s) const {
+        const __amdgpu_buffer_rsrc_t r =
+            buffer_rsrc(p.x + (size_t)u.t.start * p.K, (uint32_t)u.t.n * (uint32_t)p.K);
+        issue<kXSegs, 0>(r, xb, s, [&](int g) { return 8 * g < u.t.n ? 8 * g : -1; });
+    }
+    __device__ __forceinline__ void issue_w(const Unit &u, unsigned char *wb, int s) const {
+        const __amdgpu_buffer_rsrc_t r =
+            buffer_rsrc(p.w + ((size_t)u.t.e * p.M + u.m0) * p.K, (uint32_t)(p.M - u.m0) * (uint32_t)p.K);
+        issue<kWSegs, kAux>(r, wb, s, [&](int g) {
+            const int c = channel(8 * g);
+            return c < p.M - u.m0 ? c : -1;
+        });
+    }
+    // 64 scales per load: waves 0..4 those of the rows, waves 4..7 those of the weight rows
+    __device__ __forceinline__ void issue_scales(const Unit &u, float *to) const {
+        const int i = 64 * wave + here();
+        if (wave < kBRows / 64)
+            to_lds4(buffer_rsrc(p.x_scale + u.t.start, (uint32_t)u.t.n * 4), to + 64 * wave, i * 4);
+        if (wave >= 4) {
+            const int R = i - 256;
+            to_lds4(buffer_rsrc(p.w_scale + (size_t)u.t.e * p.M + u.m0, (uint32_t)(p.M - u.m0) * 4),
+                         to + kBRows + 64 * (wave - 4), (uint32_t)channel(R) * 4);
+        }
+    }
+    __device__ __forceinline__ void turn() const {
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's loads are in LDS
+        __syncthreads();
+    }
+
+    // The unit's products, scaled and stored; its slab 0 and scales are in LDS at entry. next() (if
+    // more): the block's next unit, whose slab 0 and scales (to nscale) are requested on the way.
+    template <int kN, class Next>
+    __device__ __forceinline__ void run(const Unit &u, Next next, bool more, const float *scale,
+                                        float *nscale) const {
+        i32x4_t acc[kBA][kN] = {};
+        const bool busy = th * kN * kTile < u.t.n;  // uniform: the wave has rows
+        auto mult = [&](const unsigned char *wb, const unsigned char *xb) __attribute__((always_inline)) {
+            if (!busy) return;
+            const int l = here(), rd = spos(l & 15, l >> 4);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                uint4 a[kBA], b[kN];
+#pragma unroll
+                for (int i = 0; i < kBA; ++i) a[i] = load16(wb + (ch * kBA + i) * kTile * kSlabB + (rd ^ 64 * s));
+#pragma unroll
+                for (int j = 0; j < kN; ++j) b[j] = load16(xb + (th * kN + j) * kTile * kSlabB + (rd ^ 64 * s));
+#pragma unroll
+                for (int j = 0; j < kN; ++j)
+#pragma unroll
+                    for (int i = 0; i < kBA; ++i) mma_i8(acc[i][j], a[i], b[j]);
+                // five subtiles: both steps' operands at once would not fit the registers
+                if constexpr (kN > 4) __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        for (int s = 0; s < nslab; s += 2) {
+            if (s + 1 < nslab) {
+                issue_x(u, b_x1, s + 1);
+                issue_w(u, b_w1, s + 1);
+            }
+            mult(b_w0, b_x0);
+            turn();
+            if (s + 2 < nslab) {
+                issue_x(u, b_x0, s + 2);
+                issue_w(u, b_w0, s + 2);
+            } else if (more) {
+                const Unit nxt = next();  // (looked up here: registers)
+                issue_x(nxt, b_x0, 0);
+                issue_w(nxt, b_w0, 0);
+                issue_scales(nxt, nscale);
+            }
+            if (s + 1 < nslab) mult(b_w1, b_x1);
+            if (s + 2 < nslab) turn();
+        }
+        __syncthreads();
+        // Results: the second weight buffer is free once every wave has left the loop. A wave turns
+        // 16 rows at a time in its 4 KB of it, so that rows leave in whole 16-byte pieces, 256
+        // bytes of a row side by side; pieces rotate by the row (no bank conflicts).
+        if (busy) {
+            constexpr int kOut = kSwiglu ? kBA / 2 : kBA;                  // output subtiles per wave
+            constexpr int kPart = 4096 / (kTile * (int)sizeof(O)) / kTile; // subtiles per turn of 4 KB
+            constexpr int kSub = kOut < kPart ? kOut : kPart;
+            constexpr int kRowB = kSub * kTile * (int)sizeof(O);           // bytes of a row per turn
+            constexpr int kPcs = kRowB / 16;                               // 16-byte pieces of it
+            const int l = here();
+            const int lc = l & 15, lq = l >> 4;
+            unsigned char *stage = b_w1 + wave * 4096;
+            const float *sw = scale + kBRows + ch * kBA * kTile + 4 * lq;
+#pragma unroll
+            for (int j = 0; j < kN; ++j) {
+                const int n0 = (th * kN + j) * kTile;
+                const float sx = scale[n0 + lc];
+#pragma unroll
+                for (int i0 = 0; i0 < kOut; i0 += kSub) {
+#pragma unroll
+                    for (int i = i0; i < i0 + kSub; ++i) {
+                        float z[4];
+                        scaled(acc[i][j], sx, sw + i * kTile, z);
+                        if constexpr (kSwiglu) {
+                            float up[4];
+                            scaled(acc[kOut + i][j], sx, sw + (kOut + i) * kTile, up);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) z[r] = silu(z[r]) * up[r];
+                        }
+                        const int at = ((i - i0) * kTile + 4 * lq) * (int)sizeof(O);
+                        store4(reinterpret_cast<O *>(stage + lc * kRowB +
+                                                     (((at >> 4) ^ lc) & (kPcs - 1)) * 16 + (at & 15)),
+                               z);
+                    }
+                    wave_exchange();
+#pragma unroll
+                    for (int g = 0; g < kTile * kPcs / kWave; ++g) {
+                        const int r = (g * kWave + l) / kPcs, pc = l & (kPcs - 1);
+                        const int m = u.m0 + (ch * kOut + i0) * kTile + pc * 16 / (int)sizeof(O);
+                        const uint4 v = load16(stage + r * kRowB + ((pc ^ r) & (kPcs - 1)) * 16);
+                        if (n0 + r < u.t.n && m < Mo)
+                            *reinterpret_cast<uint4 *>(reinterpret_cast<O *>(p.y) +
+                                                       (size_t)(u.t.start + n0 + r) * Mo + m) = v;
+                    }
+                    wave_exchange();
+                }
+            }
+        }
+        if (more) turn();  // the next unit's first slab has landed, and its second may be requested
+    }
+};
+
+// kOnce: no other row tile reads the weights (tiles of an expert are its only ones, mostly): they
+// are streamed past the caches. Units of a group of kGroup row tiles run channel block by channel
+// block, so that the 32 CUs of an XCD work on a near-square patch and share both operands in L2;
+// with weights that are read once, tile by tile.
+constexpr int kGroup = 4;
+template <bool kSwiglu, class O, bool kOnce>
+__global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(2, 2))) void i8_block_kernel(
+    I8Params p) {
+    using B = BlockProduct<kSwiglu, O, kOnce>;
+    const B b(p);
+    const int S = (b.Mo + B::kCols - 1) / B::kCols;
+    int tiles = (p.n_rows + p.tile_rows - 1) / p.tile_rows;
+    if (p.offsets) {
+        const TileScan sc = scan_tiles(p.offsets, p.E, p.n_rows, p.tile_rows);
+        tiles = sc.total;
+        if (threadIdx.x < kWave) b_scan[threadIdx.x] = sc;
+        __syncthreads();
+    }
+    // blocks b, b + 8, ... run on one XCD and share one contiguous eighth of the units, in order
+    const int units = tiles * S, per = (units + kXcds - 1) / kXcds;
+    const int first = (blockIdx.x % kXcds) * per, last = min(first + per, units);
+    auto unit = [&](int i) __attribute__((always_inline)) {
+        int ti = i / S, c = i - ti * S;
+        if (!kOnce) {
+            const int g = i / (kGroup * S), in = i - g * kGroup * S, h = min(kGroup, tiles - g * kGroup);
+            c = in / h;
+            ti = g * kGroup + in - c * h;
+        }
+        const int l = b.here();
+        return Unit{p.offsets ? pick_tile(b_scan[l], l, ti)
+                              : RowTile{0, ti * p.tile_rows, min(p.tile_rows, p.n_rows - ti * p.tile_rows)},
+                    c * B::kCols};
+    };
+    const int step = gridDim.x / kXcds;
+    int i = first + blockIdx.x / kXcds;
+    if (i >= last) return;  // uniform
+    Unit u = unit(i);
+    b.issue_x(u, b_x0, 0);
+    b.issue_w(u, b_w0, 0);
+    b.issue_scales(u, b_scale[0]);
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    __syncthreads();
+    for (int par = 0;; par ^= 1) {
+        i += step;
+        const bool more = i < last;
+        auto next = [&]() __attribute__((always_inline)) { return unit(i); };
+        const int sub = (u.t.n + 4 * kTile - 1) / (4 * kTile);  // row subtiles per wave
+        const float *scale = b_scale[par];
+        float *nscale = b_scale[par ^ 1];
+        if (sub == 1) b.template run<1>(u, next, more, scale, nscale);
+        else if (sub == 2) b.template run<2>(u, next, more, scale, nscale);
+        else if (sub == 3) b.template run<3>(u, next, more, scale, nscale);
+        else if (sub == 4) b.template run<4>(u, next, more, scale, nscale);
+        else b.template run<5>(u, next, more, scale, nscale);
+        if (!more) return;
+        u = next();
+    }
+}
+
+// ------------------------------------------------------------------------- few rows per expert
+// With a few rows per expert the time is the one read of the weights. A wave takes up to 16 kNB
+// rows of one expert and 32 weight channels (with SwiGLU 16 gate and the matching 16 up channels)
+// and streams the channels in slabs of 128 bytes, whole cache lines loaded straight into its own
+// ring of kRing slab buffers: neither registers nor a block barrier hold the stream back. The
+// rows come through buffer loads into registers in operand order; rows past the tile's read as
+// zero without a memory access, so one or two rows cost one or two lines per step.
+// kKS waves make a block and split K between them (their integer sums join in LDS, exact in any
+// order), so that a product with little to stream still spreads over the chip; where there is
+// plenty, blocks of one wave run independently and hide each other's start and end.
+constexpr int kSCh = 32, kRing = 4;
+constexpr int kSlabBytes = kSCh * kSlabB;  // one wave's slab (4 KB)
+
+template <bool kSwiglu, class O, int kNB, int kKS>
+__global__ __launch_bounds__(kKS *kWave) void i8_stream_kernel(I8Params p) {
+    // one object per ring slot, so that the compiler can tell loads into one from reads of another
+    __shared__ __align__(16) unsigned char ring0[kKS][kSlabBytes], ring1[kKS][kSlabBytes],
+        ring2[kKS][kSlabBytes], ring3[kKS][kSlabBytes];
+    constexpr int kCols = kSwiglu ? kSCh / 2 : kSCh;  // output channels of a block
+    constexpr int kRows = kTile * kNB;
+    const int lane = lane_id(), wave = kKS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
     const int col = lane & 15, q = lane >> 4;
-    const int ch = wave & 1, th = (wave >> 1) & 3;
+    auto slot = [&](auto ic) __attribute__((always_inline)) -> unsigned char * {
+        constexpr int B = decltype(ic)::value;
+        return B == 0 ? ring0[wave] : B == 1 ? ring1[wave] : B == 2 ? ring2[wave] : ring3[wave];
+    };
     const int Mo = kSwiglu ? p.M / 2 : p.M;
+    const int S = (Mo + kCols - 1) / kCols;
+    TileScan sc;
+    int tiles = (p.n_rows + kRows - 1) / kRows;
+    if (p.offsets) {
+        sc = scan_tiles(p.offsets, p.E, p.n_rows, kRows);
+        tiles = sc.total;
+    }
+    const int units = tiles * S, per = (units + kXcds - 1) / kXcds;
+    const int idx = blockIdx.x / kXcds, u = (blockIdx.x % kXcds) * per + idx;
+    if (idx >= per || u >= units) return;  // uniform
+    const int ti = u / S, m0 = (u - ti * S) * kCols;
+    const RowTile t = p.offsets ? pick_tile(sc, lane, ti)
+                                : RowTile{0, ti * kRows, min(kRows, p.n_rows - ti * kRows)};
     const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(p.x + (size_t)t.start * p.K, (uint32_t)t.n * (uint32_t)p.K);
     const __amdgpu_buffer_rsrc_t rw =
         buffer_rsrc(p.w + ((size_t)t.e * p.M + m0) * p.K, (uint32_t)(p.M - m0) * (uint32_t)p.K);
-    // weight channel (past m0) of staged row R; SwiGLU: each half of 128 staged rows holds 64 gate
-    // channels, then the 64 matching up channels
-    auto channel = [&](int R) {
-        return kSwiglu ? (R >> 7) * 64 + (R & 63) + ((R >> 6) & 1) * Mo : R;
-    };
-    const int lr = lane >> 3;
-    uint32_t xoff[kXSegs], woff[kWSegs];
-    // lane l of a segment's load writes position l % 8 of row l / 8, so it reads the piece that the
-    // row's rotation puts there: a function of the row modulo 16
-#pragma unroll
-    for (int a = 0; a < kXSegs; ++a) {
-        const int R = 8 * (kXSegs * wave + a) + lr;
-        xoff[a] = (uint32_t)R * p.K + (((lane & 7) ^ (R >> 1)) & 7) * 16;
-    }
-#pragma unroll
-    for (int a = 0; a < kWSegs; ++a) {
-        const int R = 8 * (kWSegs * wave + a) + lr;
-        woff[a] = (uint32_t)channel(R) * p.K + (((lane & 7) ^ (R >> 1)) & 7) * 16;
-    }
+    // this wave's slabs [s0, s1)
     const int nslab = (p.K + kSlabB - 1) / kSlabB;
-    const bool ragged = p.K % kSlabB != 0;
-    auto issue = [&](unsigned char *wb, unsigned char *xb, int s) __attribute__((always_inline)) {
-        const bool tail = ragged && s == nslab - 1;  // uniform
+    const int share = (nslab + kKS - 1) / kKS;
+    const int s0 = min(wave * share, nslab), s1 = min(s0 + share, nslab);
+    // segment a of a slab: staged rows 8a .. 8a + 7 (SwiGLU: rows 16 .. 31 are the up channels)
+    uint32_t woff[kSCh / 8], xoff[kNB];
+    int wk[kSCh / 8];
 #pragma unroll
-        for (int a = 0; a < kXSegs; ++a) {
-            const int R = 8 * (kXSegs * wave + a);
-            if (R >= t.n) continue;  // uniform: whole segments past the tile (their results are dropped)
-            uint32_t off = xoff[a] + s * kSlabB;
-            if (tail && s * kSlabB + (((lane & 7) ^ ((R + lr) >> 1)) & 7) * 16 >= p.K) off = kPast;
-            to_lds16(rx, xb + (kXSegs * wave + a) * 1024, off);
-        }
-#pragma unroll
-        for (int a = 0; a < kWSegs; ++a) {
-            const int R = 8 * (kWSegs * wave + a);
-            uint32_t off = woff[a] + s * kSlabB;
-            if (tail && s * kSlabB + (((lane & 7) ^ ((R + lr) >> 1)) & 7) * 16 >= p.K) off = kPast;
-            to_lds16(rw, wb + (kWSegs * wave + a) * 1024, off);
-        }
-    };
-    i32x4_t acc[kBA][kN] = {};
-    const int rd[2] = {spos(col, q), spos(col, 4 + q)};
-    const bool busy = th * kN * kTile < t.n;  // uniform: the wave has rows
-    auto mult = [&](const unsigned char *wb, const unsigned char *xb) __attribute__((always_inline)) {
-        if (!busy) return;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            uint4 a[kBA], b[kN];
-#pragma unroll
-            for (int i = 0; i < kBA; ++i) a[i] = load16(wb + (ch * kBA + i) * kTile * kSlabB + rd[s]);
-#pragma unroll
-            for (int j = 0; j < kN; ++j) b[j] = load16(xb + (th * kN + j) * kTile * kSlabB + rd[s]);
-#pragma unroll
-            for (int j = 0; j < kN; ++j)
-#pragma unroll
-                for (int i = 0; i < kBA; ++i) mma_i8(acc[i][j], a[i], b[j]);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    };
-    auto turn = [&]() __attribute__((always_inline)) {
-        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's loads are in LDS
-        __syncthreads();
-    };
-    issue(b_w0, b_x0, 0);
-    turn();
-    for (int s = 0; s < nslab; s += 2) {
-        if (s + 1 < nslab) issue(b_w1, b_x1, s + 1);
-        mult(b_w0, b_x0);
-        turn();
-        if (s + 2 < nslab) issue(b_w0, b_x0, s + 2);
-        if (s + 1 < nslab) mult(b_w1, b_x1);
-        turn();
+    for (int a = 0; a < kSCh / 8; ++a) {
+        const int R = 8 * a + (lane >> 3), c = kSwiglu ? (R & 15) + (R >> 4) * Mo : R;
+        wk[a] = (((lane & 7) ^ (R >> 1)) & 7) * 16;
+        woff[a] = (uint32_t)c * p.K + wk[a];
     }
-    if (!busy) return;
-    constexpr int kOut = kSwiglu ? kBA / 2 : kBA;
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-        const int n = (th * kN + j) * kTile + col;
+    for (int j = 0; j < kNB; ++j) xoff[j] = (uint32_t)(j * kTile + col) * p.K + q * 16;
+    uint4 xr[kRing][kNB][2];
+    // pieces at or past K, and slabs past the wave's share, read as zero
+    auto issue = [&](auto ic, int s) __attribute__((always_inline)) {
+        constexpr int B = decltype(ic)::value;
+        const int left = s < s1 ? p.K - s * kSlabB : 0;  // bytes of K from this slab on
+        const uint32_t k0 = (uint32_t)s * kSlabB;
+#pragma unroll
+        for (int a = 0; a < kSCh / 8; ++a)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rw, (__attribute__((address_space(3))) void *)(slot(ic) + a * 1024), 16,
+                (int)(wk[a] < left ? woff[a] + k0 : kPast), 0, 0, kBufNT);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < kNB; ++j)
+                xr[B][j][h] = __builtin_bit_cast(
+                    uint4, __builtin_amdgcn_raw_buffer_load_b128(
+                               rx, (int)((4 * h + q) * 16 < left ? xoff[j] + k0 + h * 64 : kPast), 0, 0));
+    };
+    i32x4_t acc[2][kNB] = {};
+    auto mult = [&](auto ic) __attribute__((always_inline)) {
+        constexpr int B = decltype(ic)::value;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint4 a[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) a[i] = load16(slot(ic) + i * kTile * kSlabB + spos(col, 4 * h + q));
+#pragma unroll
+            for (int j = 0; j < kNB; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) mma_i8(acc[i][j], a[i], xr[B][j][h]);
+        }
+    };
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    using I3 = std::integral_constant<int, 3>;
+    // loads of the three younger slabs may be outstanding when a slab is used
+    constexpr int kYoung = (kRing - 1) * (kSCh / 8 + 2 * kNB);
+    static_assert(kYoung < 64, "vmcnt has six bits");
+    constexpr int kWait = (kYoung & 15) | 0x0F70 | ((kYoung >> 4) << 14);
+    auto turn = [&](auto ic, int s) __attribute__((always_inline)) {
+        __builtin_amdgcn_s_waitcnt(kWait);
+        mult(ic);
+        issue(ic, s + kRing);
+    };
+    issue(I0{}, s0);
+    issue(I1{}, s0 + 1);
+    issue(I2{}, s0 + 2);
+    issue(I3{}, s0 + 3);
+    for (int s = s0; s < s1; s += kRing) {
+        turn(I0{}, s);
+        turn(I1{}, s + 1);
+        turn(I2{}, s + 2);
+        turn(I3{}, s + 3);
+    }
+    if constexpr (kKS > 1) {  // join the waves' sums in wave 0
+        __shared__ __align__(16) int red[kKS - 1][2][kNB][kWave][4];
+        if (wave > 0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < kNB; ++j)
+                    *reinterpret_cast<i32x4_t *>(red[wave - 1][i][j][lane]) = acc[i][j];
+        }
+        __syncthreads();
+        if (wave > 0) return;
+#pragma unroll
+        for (int w = 0; w < kKS - 1; ++w)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < kNB; ++j)
+                    acc[i][j] += *reinterpret_cast<const i32x4_t *>(red[w][i][j][lane]);
+    }
+#pragma unroll
+    for (int j = 0; j < kNB; ++j) {
+        const int n = j * kTile + col;
         if (n >= t.n) continue;
         const float sx = p.x_scale[t.start + n];
         O *y = reinterpret_cast<O *>(p.y) + (size_t)(t.start + n) * Mo;
 #pragma unroll
-        for (int i = 0; i < kOut; ++i) {
-            const int mc = m0 + (ch * kOut + i) * kTile + 4 * q;
-            if (mc >= Mo) continue;
+        for (int i = 0; i < (kSwiglu ? 1 : 2); ++i) {
+            const int mc = m0 + i * kTile + 4 * q;
+            if (mc >= Mo) continue;  // Mo is a multiple of 8: four channels are all in or all out
             const float *sw = p.w_scale + (size_t)t.e * p.M + mc;
             float z[4];
             scaled(acc[i][j], sx, sw, z);
             if constexpr (kSwiglu) {
                 float up[4];
-                scaled(acc[kOut + i][j], sx, sw + Mo, up);
+                scaled(acc[1][j], sx, sw + Mo, up);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) z[r] = z[r] / (1.0f + expf(-z[r])) * up[r];
+                for (int r = 0; r < 4; ++r) z[r] = silu(z[r]) * up[r];
             }
             store4(y + mc, z);
         }
     }
 }
 
-template <bool kSwiglu, class O>
-__global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(2, 2))) void i8_block_kernel(
-    I8Params p) {
-    constexpr int kCols = kSwiglu ? kBCh / 2 : kBCh;  // output channels of a block
-    const int Mo = kSwiglu ? p.M / 2 : p.M;
-    const int S = (Mo + kCols - 1) / kCols;
-    TileScan sc;
-    int tiles = (p.n_rows + kBRows - 1) / kBRows;
-    if (p.offsets) {
-        sc = scan_tiles(p.offsets, p.E, p.n_rows, kBRows);
-        tiles = sc.total;
+}  // namespace
+
+namespace {
+
+// CUs of the current device (looked up once per device).
+int num_cus() {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < kXcds)
+            n = 256;
+        known[dev].store(n, std::memory_order_relaxed);
     }
-    // unit = (row tile, channel block), the channel blocks of a tile next to each other; blocks
-    // b, b + 8, ... run on one XCD and take one contiguous eighth of the units
-    const int units = tiles * S, per = (units + kXcds - 1) / kXcds;
-    const int idx = blockIdx.x / kXcds, u = (blockIdx.x % kXcds) * per + idx;
-    if (idx >= per || u >= units) return;  // uniform
-    const int ti = u / S, m0 = (u - ti * S) * kCols;
-    const RowTile t = p.offsets ? pick_tile(sc, kBRows, ti)
-                                : RowTile{0, ti * kBRows, min(kBRows, p.n_rows - ti * kBRows)};
-    const int sub = (t.n + 4 * kTile - 1) / (4 * kTile);  // row subtiles per wave
-    if (sub == 1) block_product<kSwiglu, O, 1>(p, t, m0);
-    else if (sub == 2) block_product<kSwiglu, O, 2>(p, t, m0);
-    else if (sub == 3) block_product<kSwiglu, O, 3>(p, t, m0);
-    else if (sub == 4) block_product<kSwiglu, O, 4>(p, t, m0);
-    else block_product<kSwiglu, O, 5>(p, t, m0);
+    return n;
+}
+
+// The most row tiles of `per` rows that n_rows rows of E experts can make.
+long most_tiles(const I8Params &p, int per) {
+    if (!p.offsets) return (p.n_rows + per - 1) / per;
+    const long parts = p.n_rows / per + (p.E < p.n_rows ? p.E : p.n_rows);
+    return parts < p.n_rows ? parts : p.n_rows;
+}
+
+// About how many there will be: the experts' counts are on the device, so even routing is taken,
+// with half a tile more per expert once an expert has more rows than a tile.
+double likely_tiles(const I8Params &p, int per) {
+    if (!p.offsets) return (p.n_rows + per - 1) / per;
+    const double experts = p.E < p.n_rows ? p.E : p.n_rows, each = p.n_rows / experts / per;
+    return experts * (each + 0.5 > 1.0 ? each + 0.5 : 1.0);
+}
+
+// Which kernel, and how it is cut, from estimates of both in us. The constants are rates measured
+// on MI355X: stream waves take their weights and rows in at 8.5 TB/s in all, with a start and end
+// worth 12 KB each; weights come from HBM at 6 TB/s (5.6 under the block kernel's barriers); a
+// slab of the block kernel costs 1 us, from 128 rows 0.33 us and 5.5 ns a row, and a unit's end 2.5
+// us. Measured (us) where the choice turns: 256 experts of 2048 x 1024 with SwiGLU, 8 rows an
+// expert, 16-row waves 82, 32-row 86, blocks 106; 16 rows: 111, 94, 104; 24 rows: 165, 122, 102;
+// dense 4096 x 4096, 256 rows: 51, 33, 37, 512 rows: 91, 58, 39.
+struct Choice {
+    bool block;
+    int row_tiles, k_split, tile_rows;  // stream: 16-row tiles per wave, waves per block; block: rows
+};
+Choice choose(const I8Params &p, bool swiglu, int cus) {
+    const int Mo = swiglu ? p.M / 2 : p.M, nslab = (p.K + kSlabB - 1) / kSlabB;
+    const double experts = p.offsets ? (p.E < p.n_rows ? p.E : p.n_rows) : 1;
+    const double weights = experts * p.M * p.K;
+    auto most = [](double a, double b) { return a > b ? a : b; };
+    Choice c{true, 1, 1, kBRows};
+    double best = 0;
+    const int cols = swiglu ? kBCh / 2 : kBCh, S = (Mo + cols - 1) / cols;
+    // dense: the row tile whose rounds over the CUs take least; by expert: the largest (an expert's
+    // weights are read once per tile)
+    for (int r = p.offsets ? kBRows : 64; r <= kBRows; r += 64) {
+        const double rounds = ceil(likely_tiles(p, r) * S / cus);
+        const double rows = most(64, p.n_rows / experts < r ? p.n_rows / experts : r);
+        const double us = most(rounds * (nslab * most(1.0, 0.33 + 0.0055 * rows) + 2.5), weights / 5.6e6);
+        if (best == 0 || us <= best) best = us, c.tile_rows = r;
+    }
+    const int scols = swiglu ? kSCh / 2 : kSCh, SS = (Mo + scols - 1) / scols;
+    for (int nb = 1; nb <= 2; ++nb) {
+        if (most_tiles(p, nb * kTile) * SS > 1 << 24) continue;  // (grid size)
+        const double rows = p.n_rows / experts < nb * kTile ? p.n_rows / experts : nb * kTile;
+        const double waves = likely_tiles(p, nb * kTile) * SS;
+        // fewer waves than CUs: their K is split four ways
+        const int split = waves <= cus ? 4 : 1;
+        const double us = most(waves * ((kSCh + rows) * p.K + 12288) / 8.5e6,
+                               most(weights / 6.0e6, 0.35 * nslab / split));
+        if (us < best) best = us, c.block = false, c.row_tiles = nb, c.k_split = split;
+    }
+    return c;
 }
 
 }  // namespace
 
 hipError_t launch_matmul_i8(const I8Params &p, bool swiglu, int y_dtype, hipStream_t s) {
-    const int Mo = swiglu ? p.M / 2 : p.M;
-    // most row tiles n_rows rows of E experts can make: full ones, and a part of one per expert
-    const long tiles = p.offsets ? p.n_rows / kTRows + (p.E < p.n_rows ? p.E : p.n_rows)
-                                 : (p.n_rows + kTRows - 1) / kTRows;
-    if (p.n_rows >= 16 * (long)p.E) {
+    const int Mo = swiglu ? p.M / 2 : p.M, cus = num_cus();
+    const Choice c = choose(p, swiglu, cus);
+    // the output type and the epilogue
+    auto typed = [&](auto go) {
+        if (y_dtype == 0) swiglu ? go(float{}, std::true_type{}) : go(float{}, std::false_type{});
+        else swiglu ? go(uint16_t{}, std::true_type{}) : go(uint16_t{}, std::false_type{});
+    };
+    if (c.block) {
         const int cols = swiglu ? kBCh / 2 : kBCh;
-        const long t2 = p.offsets ? p.n_rows / kBRows + (p.E < p.n_rows ? p.E : p.n_rows)
-                                  : (p.n_rows + kBRows - 1) / kBRows;
-        const long grid = (t2 * ((Mo + cols - 1) / cols) + kXcds - 1) / kXcds * kXcds;
-        auto go = [&](auto o) {
+        const long units = most_tiles(p, c.tile_rows) * ((Mo + cols - 1) / cols);
+        const unsigned grid = (unsigned)((units < cus ? units : cus) + kXcds - 1) / kXcds * kXcds;
+        I8Params b = p;
+        b.tile_rows = c.tile_rows;
+        typed([&](auto o, auto glu) {
             using O = decltype(o);
-            if (swiglu) launch_k(i8_block_kernel<true, O>, (unsigned)grid, kBWaves * kWave, 0, s, p);
-            else launch_k(i8_block_kernel<false, O>, (unsigned)grid, kBWaves * kWave, 0, s, p);
-        };
-        if (y_dtype == 0) go(float{});
-        else go(uint16_t{});
+            constexpr bool kGlu = decltype(glu)::value;
+            if (p.offsets) launch_k(i8_block_kernel<kGlu, O, true>, grid, kBWaves * kWave, 0, s, b);
+            else launch_k(i8_block_kernel<kGlu, O, false>, grid, kBWaves * kWave, 0, s, b);
+        });
         return hipGetLastError();
     }
-    const long grid = tiles * ((Mo + kTCols - 1) / kTCols);
-    if (grid > 0x7FFFFFFFl) return hipErrorInvalidValue;
-    auto go = [&](auto o) {
+    const int cols = swiglu ? kSCh / 2 : kSCh;
+    const long units = most_tiles(p, c.row_tiles * kTile) * ((Mo + cols - 1) / cols);
+    const unsigned grid = (unsigned)((units + kXcds - 1) / kXcds * kXcds);
+    typed([&](auto o, auto glu) {
         using O = decltype(o);
-        if (swiglu) launch_k(i8_tile_kernel<true, O>, (unsigned)grid, 256, 0, s, p);
-        else launch_k(i8_tile_kernel<false, O>, (unsigned)grid, 256, 0, s, p);
-    };
-    if (y_dtype == 0) go(float{});
-    else go(uint16_t{});
+        constexpr bool kGlu = decltype(glu)::value;
+        if (c.row_tiles == 1 && c.k_split == 1) launch_k(i8_stream_kernel<kGlu, O, 1, 1>, grid, kWave, 0, s, p);
+        else if (c.row_tiles == 1) launch_k(i8_stream_kernel<kGlu, O, 1, 4>, grid, 4 * kWave, 0, s, p);
+        else if (c.k_split == 1) launch_k(i8_stream_kernel<kGlu, O, 2, 1>, grid, kWave, 0, s, p);
+        else launch_k(i8_stream_kernel<kGlu, O, 2, 4>, grid, 4 * kWave, 0, s, p);
+    });
     return hipGetLastError();
 }
 

@@ -167,6 +167,7 @@ struct I8Params {
     const int32_t *offsets;  // [E + 1], or nullptr: every row is expert 0's
     void *y;                 // [n_rows][M], with SwiGLU [n_rows][M / 2]
     int n_rows, E, M, K;
+    int tile_rows;           // most rows of a row tile (set by the launcher)
 };
 
 // Element types: 0 fp32, 1 bf16.

@@ -126,7 +126,7 @@ int moe_matmul_i8(const int8_t *x, const float *x_scale, int32_t n_rows, const i
     if (!rows_ok(x, n_rows) || !vec_ok(x_scale) || !rows_ok(w, 1) || !vec_ok(w_scale) ||
         !aligned(offsets, 4) || !rows_ok(y, n_rows))
         return MOE_ERR_INVALID_ARG;
-    const I8Params p{x, x_scale, w, w_scale, offsets, y, n_rows, E, M, K};
+    const I8Params p{x, x_scale, w, w_scale, offsets, y, n_rows, E, M, K, 0};
     return hip_status(launch_matmul_i8(p, swiglu != 0, y_dtype, stream));
 }
 
