@@ -279,53 +279,51 @@ class MoeLayer:
 # caller orders it after whatever writes the inputs.
 
 def _want(name, t, dtype, shape, device):
-    """t as a contiguous tensor of the dtype (or one of them), shape (None: any) and device."""
-    if not (t.dtype in dtype if isinstance(dtype, tuple) else t.dtype is dtype):
+    """Address of t, a contiguous tensor of the dtype, shape and device."""
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
     return t.data_ptr()
 
 
-def _row_types():
-    import torch
-    return torch.float32, torch.bfloat16
-
-
-def _enum(dtype):
+def _row_enum(name, dtype):
+    """The library's number of a row type."""
     import torch
     if dtype is torch.bfloat16:
         return MOE_BF16
     if dtype is torch.float32:
         return MOE_F32
-    raise ValueError(f"dtype {dtype}: torch.float32 or torch.bfloat16")
+    raise ValueError(f"{name}: dtype {dtype}, expected torch.float32 or torch.bfloat16")
 
 
 class _On:
     """Context of one call: the tensors' device current, and the given stream current on it, so
-    that what the call allocates belongs to the stream that writes it."""
+    that what the call allocates belongs to the stream that writes it. Entering gives the stream's
+    handle (read straight from torch's per-device state where nothing has to be switched: a decode
+    round's operators take a few microseconds each, and a Stream object costs three)."""
 
     def __init__(self, device, stream):
         import torch
         if device.type != "cuda":
             raise ValueError(f"tensors must be on a GPU, not on {device}")
-        self.ctx = None
+        self.device, self.ctx = device, None
         if stream is not None:
             if stream.device != device:
                 raise ValueError(f"stream of {stream.device}, tensors on {device}")
             self.ctx = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
+        elif device.index != torch._C._cuda_getDevice():
             self.ctx = torch.cuda.device(device)
 
     def __enter__(self):
         import torch
         if self.ctx is not None:
             self.ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
 
     def __exit__(self, *exc):
         if self.ctx is not None:
@@ -339,13 +337,15 @@ def permute(x, rows, n_rows=None, xs=None, stream=None):
     import torch
     T, H = x.shape
     dev = x.device
-    px, pr = _want("x", x, _row_types(), (T, H), dev), _want("rows", rows, torch.int32, (T * 8,), dev)
+    dt = x.dtype
+    num = _row_enum("x", dt)
+    px, pr = _want("x", x, dt, (T, H), dev), _want("rows", rows, torch.int32, (T * 8,), dev)
     with _On(dev, stream) as s:
         if xs is None:
-            xs = torch.empty((T * 8 if n_rows is None else n_rows, H), dtype=x.dtype, device=dev)
+            xs = torch.empty((T * 8 if n_rows is None else n_rows, H), dtype=dt, device=dev)
         n = xs.shape[0] if n_rows is None else n_rows
-        _check(load().moe_permute(px, pr, T, H, n, _enum(x.dtype),
-                                  _want("xs", xs, x.dtype, (n, H), dev), s), "moe_permute")
+        _check(load().moe_permute(px, pr, T, H, n, num, _want("xs", xs, dt, (n, H), dev), s),
+               "moe_permute")
     return xs
 
 
@@ -355,12 +355,13 @@ def permute_backward(dxs, rows, dx=None, stream=None):
     n, H = dxs.shape
     dev = dxs.device
     T = rows.numel() // 8
-    pd = _want("dxs", dxs, _row_types(), (n, H), dev)
+    num = _row_enum("dxs", dxs.dtype)
+    pd = _want("dxs", dxs, dxs.dtype, (n, H), dev)
     pr = _want("rows", rows, torch.int32, (T * 8,), dev)
     with _On(dev, stream) as s:
         if dx is None:
             dx = torch.empty((T, H), dtype=dxs.dtype, device=dev)
-        _check(load().moe_permute_backward(pd, pr, T, H, n, _enum(dxs.dtype),
+        _check(load().moe_permute_backward(pd, pr, T, H, n, num,
                                            _want("dx", dx, dxs.dtype, (T, H), dev), s),
                "moe_permute_backward")
     return dx
@@ -374,7 +375,8 @@ def unpermute(ys, rows, w, shared=None, gate=None, dtype=None, y=None, stream=No
     dev = ys.device
     T = w.shape[0]
     f32 = torch.float32
-    py = _want("ys", ys, _row_types(), (n, H), dev)
+    num = _row_enum("ys", ys.dtype)
+    py = _want("ys", ys, ys.dtype, (n, H), dev)
     pr = _want("rows", rows, torch.int32, (T * 8,), dev)
     pw = _want("w", w, f32, (T, 8), dev)
     if (shared is None) != (gate is None):
@@ -386,9 +388,9 @@ def unpermute(ys, rows, w, shared=None, gate=None, dtype=None, y=None, stream=No
             y = torch.empty((T, H), dtype=ys.dtype if dtype is None else dtype, device=dev)
         elif dtype is not None and y.dtype != dtype:
             raise ValueError(f"y: dtype {y.dtype}, expected {dtype}")
-        _check(load().moe_unpermute(py, pr, pw, ps, pg, T, H, n, _enum(ys.dtype),
-                                    _want("y", y, _row_types(), (T, H), dev), _enum(y.dtype), s),
-               "moe_unpermute")
+        _check(load().moe_unpermute(py, pr, pw, ps, pg, T, H, n, num,
+                                    _want("y", y, y.dtype, (T, H), dev), _row_enum("y", y.dtype),
+                                    s), "moe_unpermute")
     return y
 
 
@@ -400,8 +402,10 @@ def unpermute_backward(dy, ys, rows, w, shared=None, gate=None, dys=None, stream
     dev = ys.device
     T = w.shape[0]
     f32 = torch.float32
-    pd = _want("dy", dy, _row_types(), (T, H), dev)
-    py = _want("ys", ys, _row_types(), (n, H), dev)
+    dnum = _row_enum("dy", dy.dtype)
+    pd = _want("dy", dy, dy.dtype, (T, H), dev)
+    num = _row_enum("ys", ys.dtype)
+    py = _want("ys", ys, ys.dtype, (n, H), dev)
     pr = _want("rows", rows, torch.int32, (T * 8,), dev)
     pw = _want("w", w, f32, (T, 8), dev)
     if (shared is None) != (gate is None):
@@ -415,7 +419,7 @@ def unpermute_backward(dy, ys, rows, w, shared=None, gate=None, dys=None, stream
         dshared = None if shared is None else torch.empty_like(shared)
         dgate = None if shared is None else torch.empty_like(gate)
         _check(load().moe_unpermute_backward(
-            pd, py, pr, pw, ps, pg, T, H, n, _enum(ys.dtype), _enum(dy.dtype),
+            pd, py, pr, pw, ps, pg, T, H, n, num, dnum,
             _want("dys", dys, ys.dtype, (n, H), dev), dw.data_ptr(),
             None if shared is None else dshared.data_ptr(),
             None if shared is None else dgate.data_ptr(), s), "moe_unpermute_backward")
@@ -427,11 +431,12 @@ def quantize_i8(x, stream=None):
     import torch
     n, K = x.shape
     dev = x.device
-    px = _want("x", x, _row_types(), (n, K), dev)
+    num = _row_enum("x", x.dtype)
+    px = _want("x", x, x.dtype, (n, K), dev)
     with _On(dev, stream) as s:
         q = torch.empty((n, K), dtype=torch.int8, device=dev)
         scale = torch.empty((n,), dtype=torch.float32, device=dev)
-        _check(load().moe_quantize_i8(px, n, K, _enum(x.dtype), q.data_ptr(), scale.data_ptr(), s),
+        _check(load().moe_quantize_i8(px, n, K, num, q.data_ptr(), scale.data_ptr(), s),
                "moe_quantize_i8")
     return q, scale
 
@@ -444,11 +449,13 @@ def permute_i8(x, rows, n_rows=None, stream=None):
     T, H = x.shape
     dev = x.device
     n = T * 8 if n_rows is None else n_rows
-    px, pr = _want("x", x, _row_types(), (T, H), dev), _want("rows", rows, torch.int32, (T * 8,), dev)
+    dt = x.dtype
+    num = _row_enum("x", dt)
+    px, pr = _want("x", x, dt, (T, H), dev), _want("rows", rows, torch.int32, (T * 8,), dev)
     with _On(dev, stream) as s:
         q = torch.empty((n, H), dtype=torch.int8, device=dev)
         scale = torch.empty((n,), dtype=torch.float32, device=dev)
-        _check(load().moe_permute_i8(px, pr, T, H, n, _enum(x.dtype), q.data_ptr(),
+        _check(load().moe_permute_i8(px, pr, T, H, n, num, q.data_ptr(),
                                      scale.data_ptr(), s), "moe_permute_i8")
     return q, scale
 
@@ -475,8 +482,8 @@ def matmul_i8(x, x_scale, w, w_scale, offsets=None, swiglu=False, dtype=None, y=
         elif dtype is not None and y.dtype != dtype:
             raise ValueError(f"y: dtype {y.dtype}, expected {dtype}")
         _check(load().moe_matmul_i8(px, ps, n, pw, pc, E, M, K, po, int(bool(swiglu)),
-                                    _want("y", y, _row_types(), (n, Mo), dev), _enum(y.dtype), s),
-               "moe_matmul_i8")
+                                    _want("y", y, y.dtype, (n, Mo), dev), _row_enum("y", y.dtype),
+                                    s), "moe_matmul_i8")
     return y
 
 
