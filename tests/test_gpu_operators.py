@@ -467,8 +467,7 @@ def test_matmul_i8_extreme_codes():
 
 
 def test_offsets_out_of_order_stay_inside():
-    """Offsets past the rows, or falling, are clamped: nothing outside y is touched, and rows that
-    one range holds get that expert's product. Here expert 0 has rows 0..9 (from -5), experts 1 and
+    """Offsets past the rows are clamped, and where they fall nothing outside y is touched. Here expert 0 has rows 0..9 (from -5), experts 1 and
     2 none (10..10, 10..8), expert 3 rows 8..39: rows 8 and 9 are in two ranges, and either
     expert's."""
     torch = _torch()
@@ -534,6 +533,44 @@ def test_matmul_i8_past_32_bits():
     y = torch.empty((n, M), dtype=torch.float32, device="cuda")
     binding.matmul_i8(x, xs, w, ws, offsets=offsets, y=y)
     i8_check(y, x, xs, w, ws, n - 70, n, E - 1, False, "far rows")
+
+
+def test_largest_counts():
+    """The most tokens, rows and channels the entry points take, at the narrowest widths."""
+    torch = _torch()
+    T, H = 1048576, 16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    rows = torch.randperm(T * 8, generator=g, device="cuda").to(torch.int32)
+    x = torch.randn((T, H), generator=g, device="cuda").to(torch.bfloat16)
+    src = torch.empty(T * 8, dtype=torch.long, device="cuda")
+    src[rows.long()] = torch.arange(T * 8, device="cuda") // 8
+    xs = binding.permute(x, rows)
+    assert torch.equal(xs, x[src])
+    dx = binding.permute_backward(xs, rows)
+    assert torch.equal(dx, (x.double() * 8).to(torch.bfloat16))  # eight equal terms: exact
+    w = torch.full((T, 8), 0.125, device="cuda")
+    y = binding.unpermute(xs, rows, w, dtype=torch.float32)
+    assert torch.equal(y, x.float())  # eighths: exact
+    dys, dw, _, _ = binding.unpermute_backward(y, xs, rows, w)
+    assert torch.equal(dys, (xs.float() * 0.125).to(torch.bfloat16))
+    want = (x.double() ** 2).sum(1, keepdim=True).expand(T, 8)
+    check(dw, want, 1.01 * H * U * want, "dw")
+    q, s = binding.permute_i8(x, rows)
+    want_q, want_s = quantized(x)
+    assert torch.equal(q.double(), want_q[src]) and torch.equal(s, want_s[src])
+    q2, s2 = binding.quantize_i8(xs)
+    assert torch.equal(q2, q) and torch.equal(s2, s)
+    wq = torch.randint(-127, 128, (2, 8, H), generator=g, device="cuda", dtype=torch.int8)
+    ws = torch.full((2, 8), 0.01, device="cuda")
+    n = T * 8
+    offsets = torch.tensor([0, n - 5, n], dtype=torch.int32, device="cuda")
+    y = binding.matmul_i8(q, s, wq, ws, offsets=offsets, dtype=torch.float32)
+    i8_check(y, q, s, wq, ws, 0, n - 5, 0, False, "all but five")
+    i8_check(y, q, s, wq, ws, n - 5, n, 1, False, "five")
+    for rows_n in (3, 700):
+        x8, xs8, w8, ws8 = i8_case(rows_n, 32, 65536, 1, 3)
+        i8_check(binding.matmul_i8(x8, xs8, w8, ws8, swiglu=True), x8, xs8, w8, ws8, 0, rows_n, 0, True, "wide")
 
 
 # ----------------------------------------------------------------------------- tables
