@@ -331,8 +331,8 @@ struct BlockProduct {
     }
 };
 
-// kOnce: no other row tile reads the weights (tiles of an expert are its only ones, mostly): they
-// are streamed past the caches. Units of a group of kGroup row tiles run channel block by channel
+// kOnce: no other row tile reads the weights (an expert's tile is its only one, mostly): they are
+// streamed past the caches. Units of a group of kGroup row tiles run channel block by channel
 // block, so that the 32 CUs of an XCD work on a near-square patch and share both operands in L2;
 // with weights that are read once, tile by tile.
 constexpr int kGroup = 4;
@@ -582,11 +582,12 @@ double likely_tiles(const I8Params &p, int per) {
 
 // Which kernel, and how it is cut, from estimates of both in us. The constants are rates measured
 // on MI355X: stream waves take their weights and rows in at 8.5 TB/s in all, with a start and end
-// worth 12 KB each; weights come from HBM at 6 TB/s (5.6 under the block kernel's barriers); a
-// slab of the block kernel costs 1 us, from 128 rows 0.33 us and 5.5 ns a row, and a unit's end 2.5
-// us. Measured (us) where the choice turns: 256 experts of 2048 x 1024 with SwiGLU, 8 rows an
-// expert, 16-row waves 82, 32-row 86, blocks 106; 16 rows: 111, 94, 104; 24 rows: 165, 122, 102;
-// dense 4096 x 4096, 256 rows: 51, 33, 37, 512 rows: 91, 58, 39.
+// worth 8 KB each; weights come from HBM at 6 TB/s (5.2 under the block kernel's barriers); a slab
+// of the block kernel costs 1 us, from 128 rows 0.33 us and 5.5 ns a row, and a unit's end 2.5 us.
+// Measured (us) where the choice turns: 256 experts of 2048 x 1024 with SwiGLU, 8 rows an expert,
+// 16-row waves 82, 32-row 86, blocks 94; 16 rows: 111, 94, 104; 24 rows: 165, 122, 102. 256 experts
+// of 512 x 2048, 2 rows: 46, 52, 55; 6 rows 55, 61, 63, with skewed routing 39, 38, 33. Dense
+// 4096 x 4096, 256 rows: 51, 33, 37, 512 rows: 91, 58, 39.
 struct Choice {
     bool block;
     int row_tiles, k_split, tile_rows;  // stream: 16-row tiles per wave, waves per block; block: rows
@@ -604,7 +605,7 @@ Choice choose(const I8Params &p, bool swiglu, int cus) {
     for (int r = p.offsets ? kBRows : 64; r <= kBRows; r += 64) {
         const double rounds = ceil(likely_tiles(p, r) * S / cus);
         const double rows = most(64, p.n_rows / experts < r ? p.n_rows / experts : r);
-        const double us = most(rounds * (nslab * most(1.0, 0.33 + 0.0055 * rows) + 2.5), weights / 5.6e6);
+        const double us = most(rounds * (nslab * most(1.0, 0.33 + 0.0055 * rows) + 2.5), weights / 5.2e6);
         if (best == 0 || us <= best) best = us, c.tile_rows = r;
     }
     const int scols = swiglu ? kSCh / 2 : kSCh, SS = (Mo + scols - 1) / scols;
@@ -614,7 +615,7 @@ Choice choose(const I8Params &p, bool swiglu, int cus) {
         const double waves = likely_tiles(p, nb * kTile) * SS;
         // fewer waves than CUs: their K is split four ways
         const int split = waves <= cus ? 4 : 1;
-        const double us = most(waves * ((kSCh + rows) * p.K + 12288) / 8.5e6,
+        const double us = most(waves * ((kSCh + rows) * p.K + 8192) / 8.5e6,
                                most(weights / 6.0e6, 0.35 * nslab / split));
         if (us < best) best = us, c.block = false, c.row_tiles = nb, c.k_split = split;
     }
