@@ -397,11 +397,14 @@ __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(
 // ring of kRing slab buffers: neither registers nor a block barrier hold the stream back. The
 // rows come through buffer loads into registers in operand order; rows past the tile's read as
 // zero without a memory access, so one or two rows cost one or two lines per step.
+// Ten one-wave blocks fill a CU's LDS. They are persistent: a wave walks its units, and the ring
+// takes the next unit's first slabs while the last slabs and the results of the present one are
+// worked on, so that the stream does not stop between them.
 // kKS waves make a block and split K between them (their integer sums join in LDS, exact in any
-// order), so that a product with little to stream still spreads over the chip; where there is
-// plenty, blocks of one wave run independently and hide each other's start and end.
+// order) where there is so little to stream that single waves would not cover the chip.
 constexpr int kSCh = 32, kRing = 4;
 constexpr int kSlabBytes = kSCh * kSlabB;  // one wave's slab (4 KB)
+constexpr int kStreamBlocks = 10;          // one-wave blocks per CU
 
 template <bool kSwiglu, class O, int kNB, int kKS>
 __global__ __launch_bounds__(kKS *kWave) void i8_stream_kernel(I8Params p) {
@@ -425,18 +428,19 @@ __global__ __launch_bounds__(kKS *kWave) void i8_stream_kernel(I8Params p) {
         tiles = sc.total;
     }
     const int units = tiles * S, per = (units + kXcds - 1) / kXcds;
-    const int idx = blockIdx.x / kXcds, u = (blockIdx.x % kXcds) * per + idx;
-    if (idx >= per || u >= units) return;  // uniform
-    const int ti = u / S, m0 = (u - ti * S) * kCols;
-    const RowTile t = p.offsets ? pick_tile(sc, lane, ti)
-                                : RowTile{0, ti * kRows, min(kRows, p.n_rows - ti * kRows)};
-    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(p.x + (size_t)t.start * p.K, (uint32_t)t.n * (uint32_t)p.K);
-    const __amdgpu_buffer_rsrc_t rw =
-        buffer_rsrc(p.w + ((size_t)t.e * p.M + m0) * p.K, (uint32_t)(p.M - m0) * (uint32_t)p.K);
-    // this wave's slabs [s0, s1)
+    const int first = (blockIdx.x % kXcds) * per, last = min(first + per, units), step = gridDim.x / kXcds;
+    int u = first + blockIdx.x / kXcds;
+    if (u >= last) return;  // uniform
+    auto unit = [&](int i) __attribute__((always_inline)) {
+        const int ti = i / S;
+        return Unit{p.offsets ? pick_tile(sc, lane, ti)
+                              : RowTile{0, ti * kRows, min(kRows, p.n_rows - ti * kRows)},
+                    (i - ti * S) * kCols};
+    };
+    // this wave's slabs: s0 .. s0 + share - 1, in whole turns of the ring
     const int nslab = (p.K + kSlabB - 1) / kSlabB;
-    const int share = (nslab + kKS - 1) / kKS;
-    const int s0 = min(wave * share, nslab), s1 = min(s0 + share, nslab);
+    const int share = (nslab + kKS - 1) / kKS, s0 = wave * share;
+    const int turns = (share + kRing - 1) / kRing * kRing;
     // segment a of a slab: staged rows 8a .. 8a + 7 (SwiGLU: rows 16 .. 31 are the up channels)
     uint32_t woff[kSCh / 8], xoff[kNB];
     int wk[kSCh / 8];
@@ -449,16 +453,19 @@ __global__ __launch_bounds__(kKS *kWave) void i8_stream_kernel(I8Params p) {
 #pragma unroll
     for (int j = 0; j < kNB; ++j) xoff[j] = (uint32_t)(j * kTile + col) * p.K + q * 16;
     uint4 xr[kRing][kNB][2];
-    // pieces at or past K, and slabs past the wave's share, read as zero
-    auto issue = [&](auto ic, int s) __attribute__((always_inline)) {
+    // the wave's slab i of unit v: always the same number of loads (they are counted); pieces at or
+    // past K, slabs past the share and units that do not exist (any = false) read as zero
+    auto issue = [&](auto ic, const Unit &v, int i, bool any) __attribute__((always_inline)) {
         constexpr int B = decltype(ic)::value;
-        const int left = s < s1 ? p.K - s * kSlabB : 0;  // bytes of K from this slab on
-        const uint32_t k0 = (uint32_t)s * kSlabB;
+        const __amdgpu_buffer_rsrc_t rx =
+            buffer_rsrc(p.x + (size_t)v.t.start * p.K, (uint32_t)v.t.n * (uint32_t)p.K);
+        const __amdgpu_buffer_rsrc_t rw =
+            buffer_rsrc(p.w + ((size_t)v.t.e * p.M + v.m0) * p.K, (uint32_t)(p.M - v.m0) * (uint32_t)p.K);
+        const uint32_t k0 = (uint32_t)(s0 + i) * kSlabB;
+        const int left = any && i < share ? p.K - (int)k0 : 0;  // bytes of K from this slab on
 #pragma unroll
         for (int a = 0; a < kSCh / 8; ++a)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rw, (__attribute__((address_space(3))) void *)(slot(ic) + a * 1024), 16,
-                (int)(wk[a] < left ? woff[a] + k0 : kPast), 0, 0, kBufNT);
+            to_lds16<kBufNT>(rw, slot(ic) + a * 1024, wk[a] < left ? woff[a] + k0 : kPast);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -466,20 +473,6 @@ __global__ __launch_bounds__(kKS *kWave) void i8_stream_kernel(I8Params p) {
                 xr[B][j][h] = __builtin_bit_cast(
                     uint4, __builtin_amdgcn_raw_buffer_load_b128(
                                rx, (int)((4 * h + q) * 16 < left ? xoff[j] + k0 + h * 64 : kPast), 0, 0));
-    };
-    i32x4_t acc[2][kNB] = {};
-    auto mult = [&](auto ic) __attribute__((always_inline)) {
-        constexpr int B = decltype(ic)::value;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint4 a[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) a[i] = load16(slot(ic) + i * kTile * kSlabB + spos(col, 4 * h + q));
-#pragma unroll
-            for (int j = 0; j < kNB; ++j)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) mma_i8(acc[i][j], a[i], xr[B][j][h]);
-        }
     };
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
@@ -489,62 +482,104 @@ __global__ __launch_bounds__(kKS *kWave) void i8_stream_kernel(I8Params p) {
     constexpr int kYoung = (kRing - 1) * (kSCh / 8 + 2 * kNB);
     static_assert(kYoung < 64, "vmcnt has six bits");
     constexpr int kWait = (kYoung & 15) | 0x0F70 | ((kYoung >> 4) << 14);
-    auto turn = [&](auto ic, int s) __attribute__((always_inline)) {
-        __builtin_amdgcn_s_waitcnt(kWait);
-        mult(ic);
-        issue(ic, s + kRing);
-    };
-    issue(I0{}, s0);
-    issue(I1{}, s0 + 1);
-    issue(I2{}, s0 + 2);
-    issue(I3{}, s0 + 3);
-    for (int s = s0; s < s1; s += kRing) {
-        turn(I0{}, s);
-        turn(I1{}, s + 1);
-        turn(I2{}, s + 2);
-        turn(I3{}, s + 3);
-    }
-    if constexpr (kKS > 1) {  // join the waves' sums in wave 0
-        __shared__ __align__(16) int red[kKS - 1][2][kNB][kWave][4];
-        if (wave > 0) {
+
+    Unit cur = unit(u);
+    issue(I0{}, cur, 0, true);
+    issue(I1{}, cur, 1, true);
+    issue(I2{}, cur, 2, true);
+    issue(I3{}, cur, 3, true);
+    for (;;) {
+        u += step;
+        const bool more = u < last;
+        const Unit nxt = more ? unit(u) : cur;
+        // the unit's scales, requested before its products: rows and channels past it read as zero
+        // (their results are not stored)
+        float sx[kNB], sw[2][4];
+        {
+            const __amdgpu_buffer_rsrc_t r = buffer_rsrc(p.x_scale + cur.t.start, (uint32_t)cur.t.n * 4);
+            const __amdgpu_buffer_rsrc_t c =
+                buffer_rsrc(p.w_scale + (size_t)cur.t.e * p.M + cur.m0, (uint32_t)(p.M - cur.m0) * 4);
+#pragma unroll
+            for (int j = 0; j < kNB; ++j) sx[j] = __uint_as_float(bload4(r, (uint32_t)(j * kTile + col) * 4));
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < kNB; ++j)
-                    *reinterpret_cast<i32x4_t *>(red[wave - 1][i][j][lane]) = acc[i][j];
+                for (int k = 0; k < 4; ++k)
+                    sw[i][k] = __uint_as_float(bload4(c, (uint32_t)(i * (kSwiglu ? Mo : kTile) + 4 * q + k) * 4));
         }
-        __syncthreads();
-        if (wave > 0) return;
+        i32x4_t acc[2][kNB] = {};
+        auto turn = [&](auto ic, int i) __attribute__((always_inline)) {
+            constexpr int B = decltype(ic)::value;
+            __builtin_amdgcn_s_waitcnt(kWait);
 #pragma unroll
-        for (int w = 0; w < kKS - 1; ++w)
+            for (int h = 0; h < 2; ++h) {
+                uint4 a[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+                for (int k = 0; k < 2; ++k) a[k] = load16(slot(ic) + k * kTile * kSlabB + spos(col, 4 * h + q));
 #pragma unroll
                 for (int j = 0; j < kNB; ++j)
-                    acc[i][j] += *reinterpret_cast<const i32x4_t *>(red[w][i][j][lane]);
-    }
 #pragma unroll
-    for (int j = 0; j < kNB; ++j) {
-        const int n = j * kTile + col;
-        if (n >= t.n) continue;
-        const float sx = p.x_scale[t.start + n];
-        O *y = reinterpret_cast<O *>(p.y) + (size_t)(t.start + n) * Mo;
-#pragma unroll
-        for (int i = 0; i < (kSwiglu ? 1 : 2); ++i) {
-            const int mc = m0 + i * kTile + 4 * q;
-            if (mc >= Mo) continue;  // Mo is a multiple of 8: four channels are all in or all out
-            const float *sw = p.w_scale + (size_t)t.e * p.M + mc;
-            float z[4];
-            scaled(acc[i][j], sx, sw, z);
-            if constexpr (kSwiglu) {
-                float up[4];
-                scaled(acc[1][j], sx, sw + Mo, up);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) z[r] = silu(z[r]) * up[r];
+                    for (int k = 0; k < 2; ++k) mma_i8(acc[k][j], a[k], xr[B][j][h]);
             }
-            store4(y + mc, z);
+            const bool here = i + kRing < turns;  // uniform
+            issue(ic, here ? cur : nxt, here ? i + kRing : i + kRing - turns, here || more);
+        };
+        int i = 0;
+        do {
+            turn(I0{}, i);
+            turn(I1{}, i + 1);
+            turn(I2{}, i + 2);
+            turn(I3{}, i + 3);
+        } while ((i += kRing) < turns);
+        bool mine = true;
+        if constexpr (kKS > 1) {  // join the waves' sums in wave 0
+            __shared__ __align__(16) int red[kKS - 1][2][kNB][kWave][4];
+            mine = wave == 0;
+            if (!mine) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int j = 0; j < kNB; ++j)
+                        *reinterpret_cast<i32x4_t *>(red[wave - 1][k][j][lane]) = acc[k][j];
+            }
+            __syncthreads();
+            if (mine) {
+#pragma unroll
+                for (int w = 0; w < kKS - 1; ++w)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int j = 0; j < kNB; ++j)
+                            acc[k][j] += *reinterpret_cast<const i32x4_t *>(red[w][k][j][lane]);
+            }
+            if (more) __syncthreads();  // uniform: the sums are read before the next unit's are written
         }
+        if (mine) {
+#pragma unroll
+            for (int j = 0; j < kNB; ++j) {
+                const int n = j * kTile + col;
+                if (n >= cur.t.n) continue;
+                O *y = reinterpret_cast<O *>(p.y) + (size_t)(cur.t.start + n) * Mo;
+#pragma unroll
+                for (int k = 0; k < (kSwiglu ? 1 : 2); ++k) {
+                    const int mc = cur.m0 + k * kTile + 4 * q;
+                    if (mc >= Mo) continue;  // Mo is a multiple of 8: four channels are all in or all out
+                    float z[4];
+                    scaled(acc[k][j], sx[j], sw[k], z);
+                    if constexpr (kSwiglu) {
+                        float up[4];
+                        scaled(acc[1][j], sx[j], sw[1], up);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) z[r] = silu(z[r]) * up[r];
+                    }
+                    store4(y + mc, z);
+                }
+            }
+        }
+        if (!more) break;
+        cur = nxt;
     }
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // no load into this block's LDS outlives it
 }
 
 }  // namespace
@@ -582,12 +617,12 @@ double likely_tiles(const I8Params &p, int per) {
 
 // Which kernel, and how it is cut, from estimates of both in us. The constants are rates measured
 // on MI355X: stream waves take their weights and rows in at 8.5 TB/s in all, with a start and end
-// worth 8 KB each; weights come from HBM at 6 TB/s (5.2 under the block kernel's barriers); a slab
+// worth 3 KB each; weights come from HBM at 6 TB/s (5.2 under the block kernel's barriers); a slab
 // of the block kernel costs 1 us, from 128 rows 0.33 us and 5.5 ns a row, and a unit's end 2.5 us.
-// Measured (us) where the choice turns: 256 experts of 2048 x 1024 with SwiGLU, 8 rows an expert,
-// 16-row waves 82, 32-row 86, blocks 94; 16 rows: 111, 94, 104; 24 rows: 165, 122, 102. 256 experts
-// of 512 x 2048, 2 rows: 46, 52, 55; 6 rows 55, 61, 63, with skewed routing 39, 38, 33. Dense
-// 4096 x 4096, 256 rows: 51, 33, 37, 512 rows: 91, 58, 39.
+// Measured (us; 16-row waves, 32-row waves, blocks) where the choice turns: 256 experts of 2048 x
+// 1024 with SwiGLU, 8 rows an expert: 83, 86, 96; 16 rows: 111, 94, 104; 22 rows: 150, 107, 98. 256
+// experts of 512 x 2048, 6 rows: 47, 49, 63, with skewed routing 31, 30, 33; 12 rows: 61, 57, 65,
+// skewed 51, 45, 42. Dense 4096 x 4096, 256 rows: 51, 33, 37; 512 rows: 91, 58, 39.
 struct Choice {
     bool block;
     int row_tiles, k_split, tile_rows;  // stream: 16-row tiles per wave, waves per block; block: rows
@@ -610,12 +645,11 @@ Choice choose(const I8Params &p, bool swiglu, int cus) {
     }
     const int scols = swiglu ? kSCh / 2 : kSCh, SS = (Mo + scols - 1) / scols;
     for (int nb = 1; nb <= 2; ++nb) {
-        if (most_tiles(p, nb * kTile) * SS > 1 << 24) continue;  // (grid size)
         const double rows = p.n_rows / experts < nb * kTile ? p.n_rows / experts : nb * kTile;
         const double waves = likely_tiles(p, nb * kTile) * SS;
         // fewer waves than CUs: their K is split four ways
         const int split = waves <= cus ? 4 : 1;
-        const double us = most(waves * ((kSCh + rows) * p.K + 8192) / 8.5e6,
+        const double us = most(waves * ((kSCh + rows) * p.K + 3072) / 8.5e6,
                                most(weights / 6.0e6, 0.35 * nslab / split));
         if (us < best) best = us, c.block = false, c.row_tiles = nb, c.k_split = split;
     }
@@ -648,7 +682,12 @@ hipError_t launch_matmul_i8(const I8Params &p, bool swiglu, int y_dtype, hipStre
     }
     const int cols = swiglu ? kSCh / 2 : kSCh;
     const long units = most_tiles(p, c.row_tiles * kTile) * ((Mo + cols - 1) / cols);
-    const unsigned grid = (unsigned)((units + kXcds - 1) / kXcds * kXcds);
+    // a wave walks units of about 64 KB of weights in all: shorter walks pay their starts too often
+    // (512 x 2048, 2 rows an expert: 45 us for one unit a wave, 39 for four), longer ones even out
+    // badly at the end (42 for eight); more only while the chip has no room for more waves
+    const long walk = p.K < 2048 ? 2048 / p.K : 1, room = (long)cus * kStreamBlocks;
+    const long blocks = units <= room ? units : (units + walk - 1) / walk > room ? (units + walk - 1) / walk : room;
+    const unsigned grid = (unsigned)((blocks + kXcds - 1) / kXcds * kXcds);
     typed([&](auto o, auto glu) {
         using O = decltype(o);
         constexpr bool kGlu = decltype(glu)::value;
