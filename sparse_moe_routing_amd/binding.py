@@ -273,19 +273,23 @@ class MoeLayer:
 # ---------------------------------------------------------------- separate operators
 # Rows sorted by expert and back, their gradients, and products of 8-bit integers, around a
 # caller's own expert products. rows is the [T*8] int32 table of MoeLayer.bucket_rows. Tensors are
-# contiguous and on one device; what is not raises ValueError before anything is enqueued, and so
-# does a call that the library refuses (MoeError). Without `stream` the work is enqueued on the
-# tensors' device's current stream; with it, results are allocated for that stream, and the
-# caller orders it after whatever writes the inputs.
+# contiguous and on one device; what is not raises ValueError before anything is enqueued, and a
+# call that the library refuses raises MoeError. Without `stream` the work is enqueued on the
+# current stream of the tensors' device; with it, results are allocated for that stream, and the
+# caller orders it after whatever writes the inputs. A decode round's operators take a few
+# microseconds each, so this side is kept short: no Stream object (three microseconds) is made
+# where nothing has to be switched.
+_row_types = {}  # torch dtype -> the library's number (filled on first use)
 
-def _want(name, t, dtype, shape, device):
-    """Address of t, a contiguous tensor of the dtype, shape and device."""
+
+def _want(name, t, dtype, shape, index):
+    """Address of t, a contiguous tensor of the dtype and shape on GPU `index`."""
     if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -293,104 +297,101 @@ def _want(name, t, dtype, shape, device):
 
 def _row_enum(name, dtype):
     """The library's number of a row type."""
+    if not _row_types:
+        import torch
+        _row_types.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16})
+    num = _row_types.get(dtype)
+    if num is None:
+        raise ValueError(f"{name}: dtype {dtype}, expected torch.float32 or torch.bfloat16")
+    return num
+
+
+def _switched(device, stream):
+    """Context in which the tensors' device is current and, if given, the stream on it; None when
+    that is already so (and no stream is given)."""
     import torch
-    if dtype is torch.bfloat16:
-        return MOE_BF16
-    if dtype is torch.float32:
-        return MOE_F32
-    raise ValueError(f"{name}: dtype {dtype}, expected torch.float32 or torch.bfloat16")
-
-
-class _On:
-    """Context of one call: the tensors' device current, and the given stream current on it, so
-    that what the call allocates belongs to the stream that writes it. Entering gives the stream's
-    handle (read straight from torch's per-device state where nothing has to be switched: a decode
-    round's operators take a few microseconds each, and a Stream object costs three)."""
-
-    def __init__(self, device, stream):
-        import torch
-        if device.type != "cuda":
-            raise ValueError(f"tensors must be on a GPU, not on {device}")
-        self.device, self.ctx = device, None
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"stream of {stream.device}, tensors on {device}")
-            self.ctx = torch.cuda.stream(stream)
-        elif device.index != torch._C._cuda_getDevice():
-            self.ctx = torch.cuda.device(device)
-
-    def __enter__(self):
-        import torch
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.device.index)
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            return self.ctx.__exit__(*exc)
-        return None
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, not on {device}")
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream of {stream.device}, tensors on {device}")
+        return torch.cuda.stream(stream)
+    if device.index != torch._C._cuda_getDevice():
+        return torch.cuda.device(device)
+    return None
 
 
 def permute(x, rows, n_rows=None, xs=None, stream=None):
     """xs [n_rows][H] with xs[rows[8t + k]] = x[t] for x [T][H] (fp32 or bf16); n_rows: by default
     T * 8, or the rows of xs. Rows that no pair names keep what xs held."""
     import torch
-    T, H = x.shape
     dev = x.device
-    dt = x.dtype
+    ctx = _switched(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return permute(x, rows, n_rows, xs)
+    (T, H), dt, at = x.shape, x.dtype, dev.index
     num = _row_enum("x", dt)
-    px, pr = _want("x", x, dt, (T, H), dev), _want("rows", rows, torch.int32, (T * 8,), dev)
-    with _On(dev, stream) as s:
-        if xs is None:
-            xs = torch.empty((T * 8 if n_rows is None else n_rows, H), dtype=dt, device=dev)
-        n = xs.shape[0] if n_rows is None else n_rows
-        _check(load().moe_permute(px, pr, T, H, n, num, _want("xs", xs, dt, (n, H), dev), s),
-               "moe_permute")
+    px, pr = _want("x", x, dt, (T, H), at), _want("rows", rows, torch.int32, (T * 8,), at)
+    if xs is None:
+        xs = torch.empty((T * 8 if n_rows is None else n_rows, H), dtype=dt, device=dev)
+    n = xs.shape[0] if n_rows is None else n_rows
+    _check(load().moe_permute(px, pr, T, H, n, num, _want("xs", xs, dt, (n, H), at),
+                              torch._C._cuda_getCurrentRawStream(at)), "moe_permute")
     return xs
 
 
 def permute_backward(dxs, rows, dx=None, stream=None):
     """dx [T][H] with dx[t] = sum_k dxs[rows[8t + k]]: the gradient of permute."""
     import torch
-    n, H = dxs.shape
     dev = dxs.device
+    ctx = _switched(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return permute_backward(dxs, rows, dx)
+    (n, H), dt, at = dxs.shape, dxs.dtype, dev.index
     T = rows.numel() // 8
-    num = _row_enum("dxs", dxs.dtype)
-    pd = _want("dxs", dxs, dxs.dtype, (n, H), dev)
-    pr = _want("rows", rows, torch.int32, (T * 8,), dev)
-    with _On(dev, stream) as s:
-        if dx is None:
-            dx = torch.empty((T, H), dtype=dxs.dtype, device=dev)
-        _check(load().moe_permute_backward(pd, pr, T, H, n, num,
-                                           _want("dx", dx, dxs.dtype, (T, H), dev), s),
-               "moe_permute_backward")
+    num = _row_enum("dxs", dt)
+    pd, pr = _want("dxs", dxs, dt, (n, H), at), _want("rows", rows, torch.int32, (T * 8,), at)
+    if dx is None:
+        dx = torch.empty((T, H), dtype=dt, device=dev)
+    _check(load().moe_permute_backward(pd, pr, T, H, n, num, _want("dx", dx, dt, (T, H), at),
+                                       torch._C._cuda_getCurrentRawStream(at)),
+           "moe_permute_backward")
     return dx
+
+
+def _weighted(ys, rows, w, shared, gate, at):
+    """Addresses of unpermute's inputs, checked: (ys, rows, w, shared, gate)."""
+    import torch
+    if (shared is None) != (gate is None):
+        raise ValueError("shared and gate: both or neither")
+    (n, H), T = ys.shape, w.shape[0]
+    return (_want("ys", ys, ys.dtype, (n, H), at), _want("rows", rows, torch.int32, (T * 8,), at),
+            _want("w", w, torch.float32, (T, 8), at),
+            None if shared is None else _want("shared", shared, ys.dtype, (T, H), at),
+            None if gate is None else _want("gate", gate, torch.float32, (T,), at))
 
 
 def unpermute(ys, rows, w, shared=None, gate=None, dtype=None, y=None, stream=None):
     """y [T][H] with y[t] = sum_k w[t][k] ys[rows[8t + k]] + gate[t] shared[t]; y of `dtype`
     (by default that of ys)."""
     import torch
-    n, H = ys.shape
     dev = ys.device
-    T = w.shape[0]
-    f32 = torch.float32
+    ctx = _switched(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return unpermute(ys, rows, w, shared, gate, dtype, y)
+    (n, H), T, at = ys.shape, w.shape[0], dev.index
     num = _row_enum("ys", ys.dtype)
-    py = _want("ys", ys, ys.dtype, (n, H), dev)
-    pr = _want("rows", rows, torch.int32, (T * 8,), dev)
-    pw = _want("w", w, f32, (T, 8), dev)
-    if (shared is None) != (gate is None):
-        raise ValueError("shared and gate: both or neither")
-    ps = None if shared is None else _want("shared", shared, ys.dtype, (T, H), dev)
-    pg = None if gate is None else _want("gate", gate, f32, (T,), dev)
-    with _On(dev, stream) as s:
-        if y is None:
-            y = torch.empty((T, H), dtype=ys.dtype if dtype is None else dtype, device=dev)
-        elif dtype is not None and y.dtype != dtype:
-            raise ValueError(f"y: dtype {y.dtype}, expected {dtype}")
-        _check(load().moe_unpermute(py, pr, pw, ps, pg, T, H, n, num,
-                                    _want("y", y, y.dtype, (T, H), dev), _row_enum("y", y.dtype),
-                                    s), "moe_unpermute")
+    py, pr, pw, ps, pg = _weighted(ys, rows, w, shared, gate, at)
+    if y is None:
+        y = torch.empty((T, H), dtype=ys.dtype if dtype is None else dtype, device=dev)
+    elif dtype is not None and y.dtype != dtype:
+        raise ValueError(f"y: dtype {y.dtype}, expected {dtype}")
+    _check(load().moe_unpermute(py, pr, pw, ps, pg, T, H, n, num,
+                                _want("y", y, y.dtype, (T, H), at), _row_enum("y", y.dtype),
+                                torch._C._cuda_getCurrentRawStream(at)), "moe_unpermute")
     return y
 
 
@@ -398,46 +399,43 @@ def unpermute_backward(dy, ys, rows, w, shared=None, gate=None, dys=None, stream
     """(dys [n][H], dw [T][8], dshared [T][H] or None, dgate [T] or None): the gradients of
     unpermute. Rows of dys that no pair names keep what it held."""
     import torch
-    n, H = ys.shape
     dev = ys.device
-    T = w.shape[0]
-    f32 = torch.float32
-    dnum = _row_enum("dy", dy.dtype)
-    pd = _want("dy", dy, dy.dtype, (T, H), dev)
-    num = _row_enum("ys", ys.dtype)
-    py = _want("ys", ys, ys.dtype, (n, H), dev)
-    pr = _want("rows", rows, torch.int32, (T * 8,), dev)
-    pw = _want("w", w, f32, (T, 8), dev)
-    if (shared is None) != (gate is None):
-        raise ValueError("shared and gate: both or neither")
-    ps = None if shared is None else _want("shared", shared, ys.dtype, (T, H), dev)
-    pg = None if gate is None else _want("gate", gate, f32, (T,), dev)
-    with _On(dev, stream) as s:
-        if dys is None:
-            dys = torch.empty((n, H), dtype=ys.dtype, device=dev)
-        dw = torch.empty((T, 8), dtype=f32, device=dev)
-        dshared = None if shared is None else torch.empty_like(shared)
-        dgate = None if shared is None else torch.empty_like(gate)
-        _check(load().moe_unpermute_backward(
-            pd, py, pr, pw, ps, pg, T, H, n, num, dnum,
-            _want("dys", dys, ys.dtype, (n, H), dev), dw.data_ptr(),
-            None if shared is None else dshared.data_ptr(),
-            None if shared is None else dgate.data_ptr(), s), "moe_unpermute_backward")
+    ctx = _switched(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return unpermute_backward(dy, ys, rows, w, shared, gate, dys)
+    (n, H), T, at = ys.shape, w.shape[0], dev.index
+    num, dnum = _row_enum("ys", ys.dtype), _row_enum("dy", dy.dtype)
+    pd = _want("dy", dy, dy.dtype, (T, H), at)
+    py, pr, pw, ps, pg = _weighted(ys, rows, w, shared, gate, at)
+    if dys is None:
+        dys = torch.empty((n, H), dtype=ys.dtype, device=dev)
+    dw = torch.empty((T, 8), dtype=torch.float32, device=dev)
+    dshared = None if shared is None else torch.empty_like(shared)
+    dgate = None if shared is None else torch.empty_like(gate)
+    _check(load().moe_unpermute_backward(
+        pd, py, pr, pw, ps, pg, T, H, n, num, dnum, _want("dys", dys, ys.dtype, (n, H), at),
+        dw.data_ptr(), None if shared is None else dshared.data_ptr(),
+        None if shared is None else dgate.data_ptr(), torch._C._cuda_getCurrentRawStream(at)),
+        "moe_unpermute_backward")
     return dys, dw, dshared, dgate
 
 
 def quantize_i8(x, stream=None):
     """(codes [n][K] int8, scales [n] fp32) of the rows of x [n][K] (fp32 or bf16)."""
     import torch
-    n, K = x.shape
     dev = x.device
+    ctx = _switched(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return quantize_i8(x)
+    (n, K), at = x.shape, dev.index
     num = _row_enum("x", x.dtype)
-    px = _want("x", x, x.dtype, (n, K), dev)
-    with _On(dev, stream) as s:
-        q = torch.empty((n, K), dtype=torch.int8, device=dev)
-        scale = torch.empty((n,), dtype=torch.float32, device=dev)
-        _check(load().moe_quantize_i8(px, n, K, num, q.data_ptr(), scale.data_ptr(), s),
-               "moe_quantize_i8")
+    px = _want("x", x, x.dtype, (n, K), at)
+    q = torch.empty((n, K), dtype=torch.int8, device=dev)
+    scale = torch.empty((n,), dtype=torch.float32, device=dev)
+    _check(load().moe_quantize_i8(px, n, K, num, q.data_ptr(), scale.data_ptr(),
+                                  torch._C._cuda_getCurrentRawStream(at)), "moe_quantize_i8")
     return q, scale
 
 
@@ -446,17 +444,19 @@ def permute_i8(x, rows, n_rows=None, stream=None):
     as permute(x, rows) followed by quantize_i8. n_rows: by default T * 8. Rows that no pair names
     are not written."""
     import torch
-    T, H = x.shape
     dev = x.device
+    ctx = _switched(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return permute_i8(x, rows, n_rows)
+    (T, H), at = x.shape, dev.index
     n = T * 8 if n_rows is None else n_rows
-    dt = x.dtype
-    num = _row_enum("x", dt)
-    px, pr = _want("x", x, dt, (T, H), dev), _want("rows", rows, torch.int32, (T * 8,), dev)
-    with _On(dev, stream) as s:
-        q = torch.empty((n, H), dtype=torch.int8, device=dev)
-        scale = torch.empty((n,), dtype=torch.float32, device=dev)
-        _check(load().moe_permute_i8(px, pr, T, H, n, num, q.data_ptr(),
-                                     scale.data_ptr(), s), "moe_permute_i8")
+    num = _row_enum("x", x.dtype)
+    px, pr = _want("x", x, x.dtype, (T, H), at), _want("rows", rows, torch.int32, (T * 8,), at)
+    q = torch.empty((n, H), dtype=torch.int8, device=dev)
+    scale = torch.empty((n,), dtype=torch.float32, device=dev)
+    _check(load().moe_permute_i8(px, pr, T, H, n, num, q.data_ptr(), scale.data_ptr(),
+                                 torch._C._cuda_getCurrentRawStream(at)), "moe_permute_i8")
     return q, scale
 
 
@@ -467,23 +467,24 @@ def matmul_i8(x, x_scale, w, w_scale, offsets=None, swiglu=False, dtype=None, y=
     y [n][M / 2] = silu(gate) up. y of `dtype`, bf16 by default; rows of no expert keep what it
     held."""
     import torch
-    n, K = x.shape
-    E, M = w.shape[0], w.shape[1]
     dev = x.device
-    f32 = torch.float32
-    px, ps = _want("x", x, torch.int8, (n, K), dev), _want("x_scale", x_scale, f32, (n,), dev)
-    pw = _want("w", w, torch.int8, (E, M, K), dev)
-    pc = _want("w_scale", w_scale, f32, (E, M), dev)
-    po = None if offsets is None else _want("offsets", offsets, torch.int32, (E + 1,), dev)
+    ctx = _switched(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return matmul_i8(x, x_scale, w, w_scale, offsets, swiglu, dtype, y)
+    (n, K), (E, M, _), at = x.shape, w.shape, dev.index
+    i8, f32 = torch.int8, torch.float32
+    px, ps = _want("x", x, i8, (n, K), at), _want("x_scale", x_scale, f32, (n,), at)
+    pw, pc = _want("w", w, i8, (E, M, K), at), _want("w_scale", w_scale, f32, (E, M), at)
+    po = None if offsets is None else _want("offsets", offsets, torch.int32, (E + 1,), at)
     Mo = M // 2 if swiglu else M
-    with _On(dev, stream) as s:
-        if y is None:
-            y = torch.empty((n, Mo), dtype=torch.bfloat16 if dtype is None else dtype, device=dev)
-        elif dtype is not None and y.dtype != dtype:
-            raise ValueError(f"y: dtype {y.dtype}, expected {dtype}")
-        _check(load().moe_matmul_i8(px, ps, n, pw, pc, E, M, K, po, int(bool(swiglu)),
-                                    _want("y", y, y.dtype, (n, Mo), dev), _row_enum("y", y.dtype),
-                                    s), "moe_matmul_i8")
+    if y is None:
+        y = torch.empty((n, Mo), dtype=torch.bfloat16 if dtype is None else dtype, device=dev)
+    elif dtype is not None and y.dtype != dtype:
+        raise ValueError(f"y: dtype {y.dtype}, expected {dtype}")
+    _check(load().moe_matmul_i8(px, ps, n, pw, pc, E, M, K, po, 1 if swiglu else 0,
+                                _want("y", y, y.dtype, (n, Mo), at), _row_enum("y", y.dtype),
+                                torch._C._cuda_getCurrentRawStream(at)), "moe_matmul_i8")
     return y
 
 
