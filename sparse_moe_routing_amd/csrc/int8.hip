@@ -24,8 +24,8 @@ __device__ __forceinline__ void mma_i8(i32x4_t &acc, const uint4 &a, const uint4
 }
 
 // Row tiles of the experts in order: expert e's rows [lo, hi) in as few tiles of at most `per` rows
-// as hold them, of even sizes (multiples of 16 but for the last). Every wave finds tile u by itself:
-// lane l sums the tiles of experts 4l .. 4l + 3, a wave scan places them.
+// as hold them, of even sizes (multiples of 16 but for the last). Every wave finds its units by
+// itself: lane l sums the tiles of experts 4l .. 4l + 3, a wave scan places them.
 struct RowTile {
     int e, start, n;  // n = 0: there is no such tile
 };
@@ -50,25 +50,35 @@ __device__ __forceinline__ TileScan scan_tiles(const int32_t *offsets, int E, in
     s.total = __builtin_amdgcn_readlane(incl, kWave - 1);
     return s;
 }
-__device__ __forceinline__ RowTile pick_tile(const TileScan &s, int lane, int u) {
-    int at = s.at, e = 0, start = 0, n = 0;
+// One unit of work: a row tile and its first output channel.
+struct Unit {
+    RowTile t;
+    int m0;
+};
+// Unit u of S blocks of `cols` output channels per tile. An expert's units run channel block by
+// channel block, its tiles next to each other: they read the same weights at about the same time.
+__device__ __forceinline__ Unit pick_unit(const TileScan &s, int lane, int u, int S, int cols) {
+    int at = s.at, e = 0, start = 0, n = 0, c = 0;
     bool mine = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (u >= at && u < at + s.nt[i]) {
+        const int nt = s.nt[i];
+        if (u >= at * S && u < (at + nt) * S) {
             mine = true;
             e = 4 * lane + i;
-            const int rows = s.hi[i] - s.lo[i], part = ((rows + s.nt[i] - 1) / s.nt[i] + 15) & ~15;
-            start = s.lo[i] + (u - at) * part;
+            c = (u - at * S) / nt;
+            const int rows = s.hi[i] - s.lo[i], part = ((rows + nt - 1) / nt + 15) & ~15;
+            start = s.lo[i] + (u - at * S - c * nt) * part;
             n = min(part, s.hi[i] - start);
         }
-        at += s.nt[i];
+        at += nt;
     }
     const uint64_t who = __ballot(mine);
-    if (!who) return {0, 0, 0};
+    if (!who) return {{0, 0, 0}, 0};
     const int src = __ffsll((unsigned long long)who) - 1;
-    return {__builtin_amdgcn_readlane(e, src), __builtin_amdgcn_readlane(start, src),
-            __builtin_amdgcn_readlane(n, src)};
+    return {{__builtin_amdgcn_readlane(e, src), __builtin_amdgcn_readlane(start, src),
+             __builtin_amdgcn_readlane(n, src)},
+            __builtin_amdgcn_readlane(c, src) * cols};
 }
 
 __device__ __forceinline__ void store4(float *p, const float (&v)[4]) {
@@ -113,6 +123,14 @@ __device__ __forceinline__ void scaled(const i32x4_t &acc, float sx, const float
 // Bounds come from the buffer resources: the row resource covers exactly the tile's n rows and the
 // weight resource the expert's remaining channels, so that loads past either return zeros without
 // a memory access; pieces past K in the last slab are sent past the range in the same way.
+//
+// Why these sizes: per slab a CU moves 72 KB into LDS and reads 208 KB of operands for 640 matrix
+// instructions; 320 x 256 is the patch with the least LDS traffic per product whose sums still fit
+// two waves' registers, and at 65536 rows of 256 experts most experts' rows fit one tile, so that
+// their weights cross HBM once. Measured: 65536 rows of 256 experts of 2048 x 1024 with SwiGLU 178 us
+// (1.5 Pop/s; 643 MiB read, the least there is; matrix units busy 36 %, waits for operands 38 %);
+// dense 8192 x 4096 x 4096 131 us (2.1 Pop/s). 256-row tiles take 252 us where these take 229 (before
+// the last steps), 128-channel blocks 260, four waves of 128 x 128 318.
 constexpr int kBWaves = 8;
 constexpr int kBRows = 320, kBCh = 256;   // rows and weight channels per block
 constexpr int kSlabB = 128;               // bytes (K elements) of a staged row
@@ -154,12 +172,6 @@ __device__ __forceinline__ void wave_exchange() {
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
-
-// One unit: a row tile and its first output channel.
-struct Unit {
-    RowTile t;
-    int m0;
-};
 
 template <bool kSwiglu, class O, bool kOnce>
 struct BlockProduct {
@@ -331,10 +343,10 @@ struct BlockProduct {
     }
 };
 
-// kOnce: no other row tile reads the weights (an expert's tile is its only one, mostly): they are
-// streamed past the caches. Units of a group of kGroup row tiles run channel block by channel
-// block, so that the 32 CUs of an XCD work on a near-square patch and share both operands in L2;
-// with weights that are read once, tile by tile.
+// kOnce (by expert): the tiles that read an expert's weights run side by side, mostly there is one:
+// the weights are streamed past the caches. Otherwise (one matrix) the units of a group of kGroup
+// row tiles run channel block by channel block, so that the 32 CUs of an XCD work on a near-square
+// patch and share both operands in L2.
 constexpr int kGroup = 4;
 template <bool kSwiglu, class O, bool kOnce>
 __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(2, 2))) void i8_block_kernel(
@@ -353,16 +365,13 @@ __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(
     const int units = tiles * S, per = (units + kXcds - 1) / kXcds;
     const int first = (blockIdx.x % kXcds) * per, last = min(first + per, units);
     auto unit = [&](int i) __attribute__((always_inline)) {
-        int ti = i / S, c = i - ti * S;
-        if (!kOnce) {
-            const int g = i / (kGroup * S), in = i - g * kGroup * S, h = min(kGroup, tiles - g * kGroup);
-            c = in / h;
-            ti = g * kGroup + in - c * h;
+        if (p.offsets) {
+            const int l = b.here();
+            return pick_unit(b_scan[l], l, i, S, B::kCols);
         }
-        const int l = b.here();
-        return Unit{p.offsets ? pick_tile(b_scan[l], l, ti)
-                              : RowTile{0, ti * p.tile_rows, min(p.tile_rows, p.n_rows - ti * p.tile_rows)},
-                    c * B::kCols};
+        const int g = i / (kGroup * S), in = i - g * kGroup * S, h = min(kGroup, tiles - g * kGroup);
+        const int c = in / h, ti = g * kGroup + in - c * h;
+        return Unit{{0, ti * p.tile_rows, min(p.tile_rows, p.n_rows - ti * p.tile_rows)}, c * B::kCols};
     };
     const int step = gridDim.x / kXcds;
     int i = first + blockIdx.x / kXcds;
@@ -402,6 +411,9 @@ __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(
 // worked on, so that the stream does not stop between them.
 // kKS waves make a block and split K between them (their integer sums join in LDS, exact in any
 // order) where there is so little to stream that single waves would not cover the chip.
+// Measured: 256 rows over 256 experts of 2048 x 1024 with SwiGLU 53 us (6.3 TB/s of weights; plain
+// instead of non-temporal loads 63, slabs of half cache lines 65 and more); one row of 4096 x 4096 6
+// us.
 constexpr int kSCh = 32, kRing = 4;
 constexpr int kSlabBytes = kSCh * kSlabB;  // one wave's slab (4 KB)
 constexpr int kStreamBlocks = 10;          // one-wave blocks per CU
@@ -432,10 +444,9 @@ __global__ __launch_bounds__(kKS *kWave) void i8_stream_kernel(I8Params p) {
     int u = first + blockIdx.x / kXcds;
     if (u >= last) return;  // uniform
     auto unit = [&](int i) __attribute__((always_inline)) {
+        if (p.offsets) return pick_unit(sc, lane, i, S, kCols);
         const int ti = i / S;
-        return Unit{p.offsets ? pick_tile(sc, lane, ti)
-                              : RowTile{0, ti * kRows, min(kRows, p.n_rows - ti * kRows)},
-                    (i - ti * S) * kCols};
+        return Unit{{0, ti * kRows, min(kRows, p.n_rows - ti * kRows)}, (i - ti * S) * kCols};
     };
     // this wave's slabs: s0 .. s0 + share - 1, in whole turns of the ring
     const int nslab = (p.K + kSlabB - 1) / kSlabB;
@@ -620,9 +631,10 @@ double likely_tiles(const I8Params &p, int per) {
 // worth 3 KB each; weights come from HBM at 6 TB/s (5.2 under the block kernel's barriers); a slab
 // of the block kernel costs 1 us, from 128 rows 0.33 us and 5.5 ns a row, and a unit's end 2.5 us.
 // Measured (us; 16-row waves, 32-row waves, blocks) where the choice turns: 256 experts of 2048 x
-// 1024 with SwiGLU, 8 rows an expert: 83, 86, 96; 16 rows: 111, 94, 104; 22 rows: 150, 107, 98. 256
-// experts of 512 x 2048, 6 rows: 47, 49, 63, with skewed routing 31, 30, 33; 12 rows: 61, 57, 65,
-// skewed 51, 45, 42. Dense 4096 x 4096, 256 rows: 51, 33, 37; 512 rows: 91, 58, 39.
+// 1024 with SwiGLU, 8 rows an expert: 84, 86, 99; 16 rows: 119, 91, 98; 22 rows: 155, 106, 102. 256
+// experts of 512 x 2048, 6 rows: 46, 48, 63, with skewed routing 29, 29, 33; 12 rows: 57, 57, 65,
+// skewed 44, 43, 42. Dense 4096 x 4096, 64 rows: 14, 11, 37; 256 rows: 47, 30, 36; 512 rows: 87, 56,
+// 37.
 struct Choice {
     bool block;
     int row_tiles, k_split, tile_rows;  // stream: 16-row tiles per wave, waves per block; block: rows
@@ -649,7 +661,7 @@ Choice choose(const I8Params &p, bool swiglu, int cus) {
         const double waves = likely_tiles(p, nb * kTile) * SS;
         // fewer waves than CUs: their K is split four ways
         const int split = waves <= cus ? 4 : 1;
-        const double us = most(waves * ((kSCh + rows) * p.K + 3072) / 8.5e6,
+        const double us = most(waves * ((kSCh + rows) * p.K + 3000) / 8.5e6,
                                most(weights / 6.0e6, 0.35 * nslab / split));
         if (us < best) best = us, c.block = false, c.row_tiles = nb, c.k_split = split;
     }
