@@ -195,8 +195,9 @@ int moe_forward_timed(const moe_ctx *ctx, const void *x, int32_t T, const int32_
  * They need no context and no workspace, keep nothing between calls and can be captured in a HIP
  * graph. The current device must be the one that the stream and the pointers belong to. Row
  * types are MOE_F32 or MOE_BF16 (another one: MOE_ERR_INVALID_ARG). Pointers to rows are 16-byte
- * aligned, to rows/weights/scales/offsets 4-byte; matrices are row-major without gaps. Inputs and
- * outputs of one call must not overlap. T: 0..1048576 tokens, H: 8..16384, a multiple of 8.
+ * aligned, to rows/weights/scales/offsets 4-byte; matrices are row-major without gaps. An output
+ * that shares memory with an input or another output of the call is refused (MOE_ERR_INVALID_ARG);
+ * n_rows counts all rows of a sorted buffer. T: 0..1048576 tokens, H: 8..16384, a multiple of 8.
  *
  * rows [T*8] int32 (moe_bucket_rows): pair 8t + k of token t lives in row rows[8t + k] of the
  * buffers sorted by expert, which hold n_rows rows (0..8388608, the caller's capacity). A pair

@@ -220,8 +220,9 @@ class MoeLayer:
         perm = torch.empty((T * 8,), dtype=torch.int32, device=dev)
         rows = torch.empty((T * 8,), dtype=torch.int32, device=dev)
         if T == 0:  # the library enqueues nothing: no pairs
-            counts.zero_()
-            offsets.zero_()
+            with torch.cuda.stream(stream):
+                counts.zero_()
+                offsets.zero_()
         ws = self.workspace(T, dev) if ws is None else ws
         _check(self.lib.moe_bucket_rows(self.ctx, _ptr(ids), T, _ptr(counts), _ptr(offsets),
                                         _ptr(perm), _ptr(rows), _ptr(ws), ws.numel(),

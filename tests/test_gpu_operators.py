@@ -791,3 +791,40 @@ def test_graph_capture_replays(T):
             want = step()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(out, want)), r
+
+
+def test_operands_side_by_side():
+    """Operands that touch in one allocation are no overlap; one byte more in common is refused."""
+    torch = _torch()
+    T, H = 5, 64
+    rows = tables(routing(T, 16, 16, 90)[0], 16)[0]
+    room = torch.zeros((T + 8 * T + T, H), device="cuda")
+    x, xs, dx = room[:T], room[T:9 * T], room[9 * T:]
+    x.copy_(torch.randn(T, H, device="cuda"))
+    want = binding.permute(x, rows)
+    assert torch.equal(binding.permute(x, rows, xs=xs), want)
+    assert torch.equal(binding.permute_backward(xs, rows, dx=dx), binding.permute_backward(want, rows))
+    w = torch.full((T, 8), 0.125, device="cuda")
+    assert torch.equal(binding.unpermute(xs, rows, w, y=dx), binding.unpermute(want, rows, w))
+    before = room.clone()
+    for bad in (lambda: binding.permute(x, rows, xs=room[T - 1:9 * T - 1]),
+                lambda: binding.permute_backward(xs, rows, dx=room[9 * T - 1:10 * T - 1]),
+                lambda: binding.unpermute(xs, rows, w, y=room[9 * T - 1:10 * T - 1]),
+                lambda: binding.unpermute_backward(x, xs, rows, w, dys=xs)):
+        with pytest.raises(binding.MoeError):
+            bad()
+    torch.cuda.synchronize()
+    assert torch.equal(room, before)
+
+
+def test_bucket_rows_without_tokens():
+    torch = _torch()
+    from sparse_moe_routing_amd import inputs
+    m, _ = binding.layer_from_numpy(inputs.make_layer(inputs.BY_NAME["tiny_fp32_t4"]), 64)
+    ids = torch.empty((0, 8), dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    for s in (None, side):
+        counts, offsets, perm, rows = m.bucket_rows(ids, stream=s)
+        torch.cuda.synchronize()
+        assert not counts.any() and not offsets.any() and perm.numel() == rows.numel() == 0
+    m.close()

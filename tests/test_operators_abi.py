@@ -85,6 +85,34 @@ def test_nothing_to_do(lib, name):
         assert call(lib, name, n_rows=0) == MOE_OK
 
 
+OUTPUTS = {"moe_permute": ["xs"], "moe_permute_backward": ["dx"], "moe_unpermute": ["y"],
+           "moe_unpermute_backward": ["dys", "dw", "dshared", "dgate"],
+           "moe_quantize_i8": ["q", "scale"], "moe_permute_i8": ["xs", "xs_scale"],
+           "moe_matmul_i8": ["y"]}
+
+
+def overlaps():
+    for name, outs in OUTPUTS.items():
+        for out in outs:
+            for arg in GOOD[name]:
+                if arg != out and (arg in POINTERS16 | POINTERS4 or arg == "w"):
+                    yield name, out, arg
+
+
+@pytest.mark.parametrize("name,out,other", list(overlaps()))
+def test_overlap_refused(lib, name, out, other):
+    """An output that shares memory with another operand, from either side: every operand has a
+    place of its own, 16 MiB apart, but for the two. (The smallest operand takes 12 bytes.)"""
+    places = {a: A + (i << 24) for i, a in enumerate(GOOD[name])
+              if a in POINTERS16 | POINTERS4 or a == "w"}
+    last4 = 8 if out in POINTERS4 or other in POINTERS4 else 0
+    assert call(lib, name, **dict(places, **{out: places[other]})) == INV
+    if other in POINTERS4 or (other == "w" and name != "moe_matmul_i8"):
+        assert call(lib, name, **dict(places, **{other: places[out] + last4})) == INV
+    elif out in POINTERS4:
+        assert call(lib, name, **dict(places, **{out: places[other] + last4})) == INV
+
+
 def test_shared_arguments_come_together(lib):
     for name in ("moe_unpermute", "moe_unpermute_backward"):
         opt = [a for a in ("shared", "gate", "dshared", "dgate") if a in GOOD[name]]
