@@ -112,9 +112,11 @@ __device__ __forceinline__ void scaled(const i32x4_t &acc, float sx, const float
 // channels and the 128 up channels that go with them). K is staged in slabs of 128 bytes per row,
 // whole cache lines loaded straight into LDS (buffer loads with the LDS flag: no registers held
 // while in flight), double-buffered: the next slab's loads are in flight during the current slab's
-// matrix instructions, one block barrier per slab. Eight waves, two per SIMD: wave w takes the
-// channels of half w % 2 and a quarter of the tile's 16-row subtiles, at most five, so that a tile
-// of n rows costs ceil(n / 64) subtiles of matrix work per wave whatever n is.
+// matrix instructions. Eight waves, two per SIMD: wave w takes the channels of half w % 2 and a
+// quarter of the tile's 16-row subtiles, at most five, so that a tile of n rows costs ceil(n / 64)
+// subtiles of matrix work per wave whatever n is. Waves w and w + 4, on the same SIMD, run one
+// phase apart: while one reads its operands from LDS the other multiplies (65536 rows of 256
+// experts of 2048 x 1024 in a row of calls 194 us in step, 185 so; dense 8192 x 4096 x 4096 131, 126).
 //
 // A block's 144 KB of slabs leave one block per CU, so nothing else would cover a unit's start and
 // end: the blocks are persistent, one per CU, and the last slab of a unit is multiplied (and its
@@ -241,9 +243,17 @@ struct BlockProduct {
                          to + kBRows + 64 * (wave - 4), (uint32_t)channel(R) * 4);
         }
     }
-    __device__ __forceinline__ void turn() const {
-        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's loads are in LDS
-        __syncthreads();
+    // A block barrier that leaves loads in flight. kRead: after this wave's LDS reads have returned
+    // (what they read may be overwritten); kLoads: after its loads have landed in LDS.
+    template <bool kRead, bool kLoads>
+    __device__ __forceinline__ void phase_end() const {
+        if constexpr (kRead || kLoads)
+            __builtin_amdgcn_s_waitcnt((kRead ? 0x0070 : 0x0F70) | (kLoads ? 0 : 0xC00F));
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" ::: "memory");
     }
 
     // The unit's products, scaled and stored; its slab 0 and scales are in LDS at entry. next() (if
@@ -253,45 +263,72 @@ struct BlockProduct {
                                         float *nscale) const {
         i32x4_t acc[kBA][kN] = {};
         const bool busy = th * kN * kTile < u.t.n;  // uniform: the wave has rows
-        auto mult = [&](const unsigned char *wb, const unsigned char *xb) __attribute__((always_inline)) {
+        uint4 a[kBA], b[kN];
+        auto read = [&](const unsigned char *wb, const unsigned char *xb, int h) __attribute__((always_inline)) {
             if (!busy) return;
             const int l = here(), rd = spos(l & 15, l >> 4);
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                uint4 a[kBA], b[kN];
+            for (int i = 0; i < kBA; ++i) a[i] = load16(wb + (ch * kBA + i) * kTile * kSlabB + (rd ^ 64 * h));
 #pragma unroll
-                for (int i = 0; i < kBA; ++i) a[i] = load16(wb + (ch * kBA + i) * kTile * kSlabB + (rd ^ 64 * s));
-#pragma unroll
-                for (int j = 0; j < kN; ++j) b[j] = load16(xb + (th * kN + j) * kTile * kSlabB + (rd ^ 64 * s));
-#pragma unroll
-                for (int j = 0; j < kN; ++j)
-#pragma unroll
-                    for (int i = 0; i < kBA; ++i) mma_i8(acc[i][j], a[i], b[j]);
-                // five subtiles: both steps' operands at once would not fit the registers
-                if constexpr (kN > 4) __builtin_amdgcn_sched_barrier(0);
-            }
+            for (int j = 0; j < kN; ++j) b[j] = load16(xb + (th * kN + j) * kTile * kSlabB + (rd ^ 64 * h));
         };
-        for (int s = 0; s < nslab; s += 2) {
-            if (s + 1 < nslab) {
-                issue_x(u, b_x1, s + 1);
-                issue_w(u, b_w1, s + 1);
+        auto mult = [&]() __attribute__((always_inline)) {
+            if (!busy) return;
+#pragma unroll
+            for (int j = 0; j < kN; ++j)
+#pragma unroll
+                for (int i = 0; i < kBA; ++i) mma_i8(acc[i][j], a[i], b[j]);
+        };
+        // A slab in four phases (operands of each half, products of each half) that the waves of the
+        // second half of the block go through one phase later. refill() requests what comes into
+        // the slab's buffer next: after the phase in which the later waves read its second half,
+        // for both kinds of waves. The other buffer's loads were requested four phases earlier and
+        // are waited for at the same place.
+        auto slab = [&](auto late, const unsigned char *wb, const unsigned char *xb, bool there,
+                        auto refill) __attribute__((always_inline)) {
+            constexpr bool kLate = decltype(late)::value;
+            if (there) read(wb, xb, 0);
+            phase_end<true, false>();
+            if (there) mult();
+            phase_end<false, false>();
+            if (there) read(wb, xb, 1);
+            phase_end<true, kLate>();
+            if (kLate) refill();
+            if (there) mult();
+            phase_end<false, !kLate>();
+            if (!kLate) refill();
+        };
+        auto slabs = [&](auto late) __attribute__((always_inline)) {
+            constexpr bool kLate = decltype(late)::value;
+            if (kLate) phase_end<false, false>();
+            for (int s = 0; s < nslab; s += 2) {
+                slab(late, b_w0, b_x0, true, [&]() __attribute__((always_inline)) {
+                    if (s + 2 < nslab) {
+                        issue_x(u, b_x0, s + 2);
+                        issue_w(u, b_w0, s + 2);
+                    } else if (more) {
+                        const Unit nxt = next();  // (looked up here: registers)
+                        issue_x(nxt, b_x0, 0);
+                        issue_w(nxt, b_w0, 0);
+                        issue_scales(nxt, nscale);
+                    }
+                });
+                slab(late, b_w1, b_x1, s + 1 < nslab, [&]() __attribute__((always_inline)) {
+                    if (s + 3 < nslab) {
+                        issue_x(u, b_x1, s + 3);
+                        issue_w(u, b_w1, s + 3);
+                    }
+                });
             }
-            mult(b_w0, b_x0);
-            turn();
-            if (s + 2 < nslab) {
-                issue_x(u, b_x0, s + 2);
-                issue_w(u, b_w0, s + 2);
-            } else if (more) {
-                const Unit nxt = next();  // (looked up here: registers)
-                issue_x(nxt, b_x0, 0);
-                issue_w(nxt, b_w0, 0);
-                issue_scales(nxt, nscale);
-            }
-            if (s + 1 < nslab) mult(b_w1, b_x1);
-            if (s + 2 < nslab) turn();
+            if (!kLate) phase_end<false, false>();  // both kinds end together
+        };
+        if (1 < nslab) {
+            issue_x(u, b_x1, 1);
+            issue_w(u, b_w1, 1);
         }
-        __syncthreads();
-        // Results: the second weight buffer is free once every wave has left the loop. A wave turns
+        if (wave >= kBWaves / 2) slabs(std::true_type{});
+        else slabs(std::false_type{});
+        // Results: the second weight buffer is free now, the next unit's first slab has landed. A wave turns
         // 16 rows at a time in its 4 KB of it, so that rows leave in whole 16-byte pieces, 256
         // bytes of a row side by side; pieces rotate by the row (no bank conflicts).
         if (busy) {
@@ -339,7 +376,7 @@ struct BlockProduct {
                 }
             }
         }
-        if (more) turn();  // the next unit's first slab has landed, and its second may be requested
+        phase_end<true, false>();  // the second buffers may be filled again
     }
 };
 
