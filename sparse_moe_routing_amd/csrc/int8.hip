@@ -108,7 +108,7 @@ __device__ __forceinline__ void scaled(const i32x4_t &acc, float sx, const float
 }
 
 // ------------------------------------------------------------------------- large row counts
-// A block multiplies up to 320 rows of one expert by 256 weight channels (with SwiGLU: 128 gate
+// The wide form: a block multiplies up to 320 rows of one expert by 256 weight channels (with SwiGLU: 128 gate
 // channels and the 128 up channels that go with them). K is staged in slabs of 128 bytes per row,
 // whole cache lines loaded straight into LDS (buffer loads with the LDS flag: no registers held
 // while in flight), double-buffered: the next slab's loads are in flight during the current slab's
@@ -133,11 +133,19 @@ __device__ __forceinline__ void scaled(const i32x4_t &acc, float sx, const float
 // (1.5 Pop/s; 643 MiB read, the least there is; matrix units busy 36 %, waits for operands 38 %);
 // dense 8192 x 4096 x 4096 131 us (2.1 Pop/s). 256-row tiles take 252 us where these take 229 (before
 // the last steps), 128-channel blocks 260, four waves of 128 x 128 318.
+//
+// With fewer rows per expert a slab's matrix work is over long before the next slab has landed, and
+// one slab ahead is not enough to keep the weights coming. The deep form (kDeep) takes at most 128
+// rows a tile; the LDS saved holds a third pair of slab buffers, so that two slabs are in flight
+// behind the one in use. A wave counts its loads (always the same number per slab, past the operands
+// they read zero), waits for all but the youngest slab's, and there is one barrier per slab. Measured,
+// 256 experts of 2048 x 1024 with SwiGLU, 31 rows each: 94 us (6.2 TB/s; the wide form 110), skewed
+// 67 (90); dense 512 x 4096 x 4096 27 (39).
 constexpr int kBWaves = 8;
 constexpr int kBRows = 320, kBCh = 256;   // rows and weight channels per block
 constexpr int kSlabB = 128;               // bytes (K elements) of a staged row
 constexpr int kBA = kBCh / 2 / kTile;     // channel subtiles per wave (8)
-constexpr int kXSegs = kBRows * kSlabB / 1024 / kBWaves;  // 1 KB row segments per wave (5)
+constexpr int kDeepRows = 128;            // rows per block of the deep form
 constexpr int kWSegs = kBCh * kSlabB / 1024 / kBWaves;    // 1 KB weight segments per wave (4)
 constexpr int kXcds = 8;
 constexpr uint32_t kPast = 0xFFFFFFF0u;   // a buffer offset past every range
@@ -151,6 +159,10 @@ __device__ __forceinline__ int spos(int r, int pc) { return r * kSlabB + ((pc ^ 
 // reads of the other.
 __shared__ __align__(16) unsigned char b_w0[kBCh * kSlabB], b_w1[kBCh * kSlabB];
 __shared__ __align__(16) unsigned char b_x0[kBRows * kSlabB], b_x1[kBRows * kSlabB];
+// The deep form's three.
+__shared__ __align__(16) unsigned char d_w0[kBCh * kSlabB], d_w1[kBCh * kSlabB], d_w2[kBCh * kSlabB];
+__shared__ __align__(16) unsigned char d_x0[kDeepRows * kSlabB], d_x1[kDeepRows * kSlabB],
+    d_x2[kDeepRows * kSlabB];
 // Scales of the current and the next unit: rows, then staged weight rows.
 __shared__ __align__(16) float b_scale[2][kBRows + kBCh];
 
@@ -175,8 +187,10 @@ __device__ __forceinline__ void wave_exchange() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-template <bool kSwiglu, class O, bool kOnce>
+template <bool kSwiglu, class O, bool kOnce, bool kDeep>
 struct BlockProduct {
+    static constexpr int kXSegs = (kDeep ? kDeepRows : kBRows) * kSlabB / 1024 / kBWaves;  // 1 KB row segments
+                                                                                           // per wave
     static constexpr int kCols = kSwiglu ? kBCh / 2 : kBCh;  // output channels of a block
     static constexpr int kAux = kOnce ? kBufNT : 0;          // cache policy of the weights
     const I8Params &p;
@@ -215,21 +229,21 @@ struct BlockProduct {
 #pragma unroll
         for (int a = 0; a < kSegs; ++a) {
             const int g = kSegs * wave + a, first = row(g);
-            if (first >= 0)  // uniform
+            if (kDeep || first >= 0)  // uniform; the deep form counts its loads, past the operand they read zero
                 to_lds16<kAuxBits>(r, buf + g * 1024, (g & 1 ? odd : even) + (uint32_t)(first * p.K + s * kSlabB));
         }
     }
     __device__ __forceinline__ void issue_x(const Unit &u, unsigned char *xb, int s) const {
         const __amdgpu_buffer_rsrc_t r =
             buffer_rsrc(p.x + (size_t)u.t.start * p.K, (uint32_t)u.t.n * (uint32_t)p.K);
-        issue<kXSegs, 0>(r, xb, s, [&](int g) { return 8 * g < u.t.n ? 8 * g : -1; });
+        issue<kXSegs, 0>(r, xb, s, [&](int g) { return kDeep || 8 * g < u.t.n ? 8 * g : -1; });
     }
     __device__ __forceinline__ void issue_w(const Unit &u, unsigned char *wb, int s) const {
         const __amdgpu_buffer_rsrc_t r =
             buffer_rsrc(p.w + ((size_t)u.t.e * p.M + u.m0) * p.K, (uint32_t)(p.M - u.m0) * (uint32_t)p.K);
         issue<kWSegs, kAux>(r, wb, s, [&](int g) {
             const int c = channel(8 * g);
-            return c < p.M - u.m0 ? c : -1;
+            return kDeep || c < p.M - u.m0 ? c : -1;
         });
     }
     // 64 scales per load: waves 0..4 those of the rows, waves 4..7 those of the weight rows
@@ -245,10 +259,12 @@ struct BlockProduct {
     }
     // A block barrier that leaves loads in flight. kRead: after this wave's LDS reads have returned
     // (what they read may be overwritten); kLoads: after its loads have landed in LDS.
-    template <bool kRead, bool kLoads>
+    // kYoung: all but this many of them.
+    template <bool kRead, bool kLoads, int kYoung = 0>
     __device__ __forceinline__ void phase_end() const {
+        static_assert(kYoung < 16, "the counter's low bits");
         if constexpr (kRead || kLoads)
-            __builtin_amdgcn_s_waitcnt((kRead ? 0x0070 : 0x0F70) | (kLoads ? 0 : 0xC00F));
+            __builtin_amdgcn_s_waitcnt((kRead ? 0x0070 : 0x0F70) | (kLoads ? kYoung : 0xC00F));
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_barrier();
@@ -265,7 +281,7 @@ struct BlockProduct {
         const bool busy = th * kN * kTile < u.t.n;  // uniform: the wave has rows
         uint4 a[kBA], b[kN];
         auto read = [&](const unsigned char *wb, const unsigned char *xb, int h) __attribute__((always_inline)) {
-            if (!busy) return;
+            if (!kDeep && !busy) return;
             const int l = here(), rd = spos(l & 15, l >> 4);
 #pragma unroll
             for (int i = 0; i < kBA; ++i) a[i] = load16(wb + (ch * kBA + i) * kTile * kSlabB + (rd ^ 64 * h));
@@ -273,7 +289,7 @@ struct BlockProduct {
             for (int j = 0; j < kN; ++j) b[j] = load16(xb + (th * kN + j) * kTile * kSlabB + (rd ^ 64 * h));
         };
         auto mult = [&]() __attribute__((always_inline)) {
-            if (!busy) return;
+            if (!kDeep && !busy) return;
 #pragma unroll
             for (int j = 0; j < kN; ++j)
 #pragma unroll
@@ -297,6 +313,48 @@ struct BlockProduct {
             if (there) mult();
             phase_end<false, !kLate>();
             if (!kLate) refill();
+        };
+        // The deep form: three buffers, two slabs ahead, a barrier per slab. Slab s of a turn of three
+        // lies in buffer s % 3; in a unit's last turn the first two buffers take the next unit's
+        // first slabs, the third is left for the results.
+        auto deep = [&]() __attribute__((always_inline)) {
+            constexpr int kLoads = kXSegs + kWSegs;  // loads of a slab
+            issue_x(u, d_x2, 2);
+            issue_w(u, d_w2, 2);
+            Unit nxt = u;
+            if (more) nxt = next();
+            auto work = [&](const unsigned char *wb, const unsigned char *xb) __attribute__((always_inline)) {
+                read(wb, xb, 0);
+                mult();
+                read(wb, xb, 1);
+                mult();
+            };
+            auto fill = [&](const Unit &v, unsigned char *wb, unsigned char *xb, int s, bool any)
+                            __attribute__((always_inline)) {
+                issue_x(v, xb, any ? s : nslab);  // (past K: zeros)
+                issue_w(v, wb, any ? s : nslab);
+            };
+            int s = 0;
+            for (; s + 3 < nslab; s += 3) {
+                work(d_w0, d_x0);
+                phase_end<true, true, kLoads>();
+                fill(u, d_w0, d_x0, s + 3, true);
+                work(d_w1, d_x1);
+                phase_end<true, true, kLoads>();
+                fill(u, d_w1, d_x1, s + 4, true);
+                work(d_w2, d_x2);
+                phase_end<true, true, kLoads>();
+                fill(u, d_w2, d_x2, s + 5, true);
+            }
+            work(d_w0, d_x0);
+            phase_end<true, true, kLoads>();
+            issue_scales(nxt, nscale);
+            fill(nxt, d_w0, d_x0, 0, more);
+            if (s + 1 < nslab) work(d_w1, d_x1);
+            phase_end<true, true, kLoads>();
+            fill(nxt, d_w1, d_x1, 1, more);
+            if (s + 2 < nslab) work(d_w2, d_x2);
+            phase_end<true, true, kLoads>();
         };
         auto slabs = [&](auto late) __attribute__((always_inline)) {
             constexpr bool kLate = decltype(late)::value;
@@ -322,12 +380,25 @@ struct BlockProduct {
             }
             if (!kLate) phase_end<false, false>();  // both kinds end together
         };
-        if (1 < nslab) {
-            issue_x(u, b_x1, 1);
-            issue_w(u, b_w1, 1);
+        // the deep form takes its scales to registers here: later the next unit's are on their way
+        float sxs[kN], sws[kBA][4];
+        if constexpr (kDeep) {
+            const int l = here();
+#pragma unroll
+            for (int j = 0; j < kN; ++j) sxs[j] = scale[(th * kN + j) * kTile + (l & 15)];
+#pragma unroll
+            for (int i = 0; i < kBA; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sws[i][r] = scale[kBRows + (ch * kBA + i) * kTile + 4 * (l >> 4) + r];
+            deep();
+        } else {
+            if (1 < nslab) {
+                issue_x(u, b_x1, 1);
+                issue_w(u, b_w1, 1);
+            }
+            if (wave >= kBWaves / 2) slabs(std::true_type{});
+            else slabs(std::false_type{});
         }
-        if (wave >= kBWaves / 2) slabs(std::true_type{});
-        else slabs(std::false_type{});
         // Results: the second weight buffer is free now, the next unit's first slab has landed. A wave turns
         // 16 rows at a time in its 4 KB of it, so that rows leave in whole 16-byte pieces, 256
         // bytes of a row side by side; pieces rotate by the row (no bank conflicts).
@@ -339,21 +410,21 @@ struct BlockProduct {
             constexpr int kPcs = kRowB / 16;                               // 16-byte pieces of it
             const int l = here();
             const int lc = l & 15, lq = l >> 4;
-            unsigned char *stage = b_w1 + wave * 4096;
+            unsigned char *stage = (kDeep ? d_w2 : b_w1) + wave * 4096;
             const float *sw = scale + kBRows + ch * kBA * kTile + 4 * lq;
 #pragma unroll
             for (int j = 0; j < kN; ++j) {
                 const int n0 = (th * kN + j) * kTile;
-                const float sx = scale[n0 + lc];
+                const float sx = kDeep ? sxs[j] : scale[n0 + lc];
 #pragma unroll
                 for (int i0 = 0; i0 < kOut; i0 += kSub) {
 #pragma unroll
                     for (int i = i0; i < i0 + kSub; ++i) {
                         float z[4];
-                        scaled(acc[i][j], sx, sw + i * kTile, z);
+                        scaled(acc[i][j], sx, kDeep ? sws[i] : sw + i * kTile, z);
                         if constexpr (kSwiglu) {
                             float up[4];
-                            scaled(acc[kOut + i][j], sx, sw + (kOut + i) * kTile, up);
+                            scaled(acc[kOut + i][j], sx, kDeep ? sws[kOut + i] : sw + (kOut + i) * kTile, up);
 #pragma unroll
                             for (int r = 0; r < 4; ++r) z[r] = silu(z[r]) * up[r];
                         }
@@ -385,10 +456,10 @@ struct BlockProduct {
 // row tiles run channel block by channel block, so that the 32 CUs of an XCD work on a near-square
 // patch and share both operands in L2.
 constexpr int kGroup = 4;
-template <bool kSwiglu, class O, bool kOnce>
+template <bool kSwiglu, class O, bool kOnce, bool kDeep>
 __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(2, 2))) void i8_block_kernel(
     I8Params p) {
-    using B = BlockProduct<kSwiglu, O, kOnce>;
+    using B = BlockProduct<kSwiglu, O, kOnce, kDeep>;
     const B b(p);
     const int S = (b.Mo + B::kCols - 1) / B::kCols;
     int tiles = (p.n_rows + p.tile_rows - 1) / p.tile_rows;
@@ -414,11 +485,14 @@ __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(
     int i = first + blockIdx.x / kXcds;
     if (i >= last) return;  // uniform
     Unit u = unit(i);
-    b.issue_x(u, b_x0, 0);
-    b.issue_w(u, b_w0, 0);
     b.issue_scales(u, b_scale[0]);
-    __builtin_amdgcn_s_waitcnt(0x0F70);
-    __syncthreads();
+    b.issue_x(u, kDeep ? d_x0 : b_x0, 0);
+    b.issue_w(u, kDeep ? d_w0 : b_w0, 0);
+    if constexpr (kDeep) {
+        b.issue_x(u, d_x1, 1);
+        b.issue_w(u, d_w1, 1);
+    }
+    b.template phase_end<true, true, kDeep ? B::kXSegs + kWSegs : 0>();
     for (int par = 0;; par ^= 1) {
         i += step;
         const bool more = i < last;
@@ -427,13 +501,15 @@ __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(
         const float *scale = b_scale[par];
         float *nscale = b_scale[par ^ 1];
         if (sub == 1) b.template run<1>(u, next, more, scale, nscale);
-        else if (sub == 2) b.template run<2>(u, next, more, scale, nscale);
+        else if (kDeep || sub == 2) b.template run<2>(u, next, more, scale, nscale);
+        else if constexpr (kDeep) return;  // (not reached)
         else if (sub == 3) b.template run<3>(u, next, more, scale, nscale);
         else if (sub == 4) b.template run<4>(u, next, more, scale, nscale);
         else b.template run<5>(u, next, more, scale, nscale);
-        if (!more) return;
+        if (!more) break;
         u = next();
     }
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // no load into this block's LDS outlives it
 }
 
 // ------------------------------------------------------------------------- few rows per expert
@@ -655,51 +731,55 @@ long most_tiles(const I8Params &p, int per) {
     return parts < p.n_rows ? parts : p.n_rows;
 }
 
-// About how many there will be: the experts' counts are on the device, so even routing is taken,
-// with half a tile more per expert once an expert has more rows than a tile.
-double likely_tiles(const I8Params &p, int per) {
+// About how many there will be: the experts' counts are on the device, so even routing is taken, and
+// `more` of a tile more per expert once its rows come near a tile's.
+double likely_tiles(const I8Params &p, int per, double more) {
     if (!p.offsets) return (p.n_rows + per - 1) / per;
     const double experts = p.E < p.n_rows ? p.E : p.n_rows, each = p.n_rows / experts / per;
-    return experts * (each + 0.5 > 1.0 ? each + 0.5 : 1.0);
+    return experts * (each + more > 1.0 ? each + more : 1.0);
 }
 
-// Which kernel, and how it is cut, from estimates of both in us. The constants are rates measured
-// on MI355X: stream waves take their weights and rows in at 8.5 TB/s in all, with a start and end
-// worth 3 KB each; weights come from HBM at 6 TB/s (5.2 under the block kernel's barriers); a slab
-// of the block kernel costs 1 us, from 128 rows 0.33 us and 5.5 ns a row, and a unit's end 2.5 us.
-// Measured (us; 16-row waves, 32-row waves, blocks) where the choice turns: 256 experts of 2048 x
-// 1024 with SwiGLU, 8 rows an expert: 84, 86, 99; 16 rows: 119, 91, 98; 22 rows: 155, 106, 102. 256
-// experts of 512 x 2048, 6 rows: 46, 48, 63, with skewed routing 29, 29, 33; 12 rows: 57, 57, 65,
-// skewed 44, 43, 42. Dense 4096 x 4096, 64 rows: 14, 11, 37; 256 rows: 47, 30, 36; 512 rows: 87, 56,
-// 37.
+// Which kernel, and how it is cut, from estimates of all in us. The constants are rates measured on
+// MI355X. Stream waves take their weights and rows in at 8.5 TB/s in all, with a start and end worth
+// 3 KB each. HBM gives 6.4 TB/s to them, 6.1 to the deep block form and 5.2 to the wide one, and an
+// expert's weights are read once per tile. A slab of a block costs 0.33 us and 5.5 ns a row, at
+// least 0.78 (deep) or 1.2 (wide); a unit's end 2 us and its results' stores.
+// Measured where the choice turns (us; the better of 16- and 32-row waves, deep, wide): 256 experts
+// of 2048 x 1024 with SwiGLU, even routing, 6 rows an expert: 82, 88, 97; 12 rows: 91, 90, 99; 31
+// rows: 149, 94, 110; 94 rows: deep 117, wide 124; 144 rows: 199, 140. The same with skewed routing,
+// where hot experts have many tiles: 46, 45, 54; 68, 48, 62; 120, 66, 89; 111, 125; 152, 148. Dense
+// 4096 x 4096, 128 rows: 16, 27, 41; 256 rows: 30, 27, 42; 2048 rows: deep 41, wide 48; 4096 rows:
+// 76, 64.
 struct Choice {
     bool block;
     int row_tiles, k_split, tile_rows;  // stream: 16-row tiles per wave, waves per block; block: rows
 };
-Choice choose(const I8Params &p, bool swiglu, int cus) {
+Choice choose(const I8Params &p, bool swiglu, int out_bytes, int cus) {
     const int Mo = swiglu ? p.M / 2 : p.M, nslab = (p.K + kSlabB - 1) / kSlabB;
     const double experts = p.offsets ? (p.E < p.n_rows ? p.E : p.n_rows) : 1;
-    const double weights = experts * p.M * p.K;
+    const double weights = (double)p.M * p.K, rows = p.n_rows / experts;
+    const double others = (double)p.n_rows * (p.K + (double)Mo * out_bytes);
     auto most = [](double a, double b) { return a > b ? a : b; };
+    auto least = [](double a, double b) { return a < b ? a : b; };
     Choice c{true, 1, 1, kBRows};
     double best = 0;
     const int cols = swiglu ? kBCh / 2 : kBCh, S = (Mo + cols - 1) / cols;
-    // dense: the row tile whose rounds over the CUs take least; by expert: the largest (an expert's
-    // weights are read once per tile)
-    for (int r = p.offsets ? kBRows : 64; r <= kBRows; r += 64) {
-        const double rounds = ceil(likely_tiles(p, r) * S / cus);
-        const double rows = most(64, p.n_rows / experts < r ? p.n_rows / experts : r);
-        const double us = most(rounds * (nslab * most(1.0, 0.33 + 0.0055 * rows) + 2.5), weights / 5.2e6);
+    // dense: the row tile whose rounds over the CUs take least; by expert: the largest of either form
+    for (int r = p.offsets ? kDeepRows : 64; r <= kBRows; r += p.offsets ? kBRows - kDeepRows : 64) {
+        const bool deep = r <= kDeepRows;
+        const double tiles = likely_tiles(p, r, 0.35), n = least(rows, r);
+        const double unit = nslab * most(deep ? 0.78 : 1.2, 0.33 + 0.0055 * n) + 2.0 + n * cols * out_bytes / 22e3;
+        const double reads = (p.offsets ? tiles : 1.0) * weights + others;
+        const double us = most(ceil(tiles * S / cus) * unit, reads / (deep ? 6.1e6 : 5.2e6));
         if (best == 0 || us <= best) best = us, c.tile_rows = r;
     }
     const int scols = swiglu ? kSCh / 2 : kSCh, SS = (Mo + scols - 1) / scols;
     for (int nb = 1; nb <= 2; ++nb) {
-        const double rows = p.n_rows / experts < nb * kTile ? p.n_rows / experts : nb * kTile;
-        const double waves = likely_tiles(p, nb * kTile) * SS;
+        const double waves = likely_tiles(p, nb * kTile, nb == 1 ? 0.6 : 0.75) * SS;
         // fewer waves than CUs: their K is split four ways
         const int split = waves <= cus ? 4 : 1;
-        const double us = most(waves * ((kSCh + rows) * p.K + 3000) / 8.5e6,
-                               most(weights / 6.0e6, 0.35 * nslab / split));
+        const double us = most(waves * ((kSCh + least(rows, nb * kTile)) * p.K + 3000) / 8.5e6,
+                               most(experts * weights / 6.4e6, 0.35 * nslab / split));
         if (us < best) best = us, c.block = false, c.row_tiles = nb, c.k_split = split;
     }
     return c;
@@ -709,7 +789,7 @@ Choice choose(const I8Params &p, bool swiglu, int cus) {
 
 hipError_t launch_matmul_i8(const I8Params &p, bool swiglu, int y_dtype, hipStream_t s) {
     const int Mo = swiglu ? p.M / 2 : p.M, cus = num_cus();
-    const Choice c = choose(p, swiglu, cus);
+    const Choice c = choose(p, swiglu, y_dtype == 0 ? 4 : 2, cus);
     // the output type and the epilogue
     auto typed = [&](auto go) {
         if (y_dtype == 0) swiglu ? go(float{}, std::true_type{}) : go(float{}, std::false_type{});
@@ -724,8 +804,11 @@ hipError_t launch_matmul_i8(const I8Params &p, bool swiglu, int y_dtype, hipStre
         typed([&](auto o, auto glu) {
             using O = decltype(o);
             constexpr bool kGlu = decltype(glu)::value;
-            if (p.offsets) launch_k(i8_block_kernel<kGlu, O, true>, grid, kBWaves * kWave, 0, s, b);
-            else launch_k(i8_block_kernel<kGlu, O, false>, grid, kBWaves * kWave, 0, s, b);
+            const bool deep = c.tile_rows <= kDeepRows;
+            if (p.offsets && deep) launch_k(i8_block_kernel<kGlu, O, true, true>, grid, kBWaves * kWave, 0, s, b);
+            else if (p.offsets) launch_k(i8_block_kernel<kGlu, O, true, false>, grid, kBWaves * kWave, 0, s, b);
+            else if (deep) launch_k(i8_block_kernel<kGlu, O, false, true>, grid, kBWaves * kWave, 0, s, b);
+            else launch_k(i8_block_kernel<kGlu, O, false, false>, grid, kBWaves * kWave, 0, s, b);
         });
         return hipGetLastError();
     }
