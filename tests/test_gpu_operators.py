@@ -428,6 +428,43 @@ def test_matmul_i8_dense(n, K, M, swiglu, out):
     i8_check(y, x, xs, w, ws, 0, n, 0, swiglu, (n, K, M))
 
 
+# enough rows that blocks of 128 or 320 rows multiply them: K of 1 to 8 slabs of 128, whole and not,
+# M in whole and partial channel blocks, tiles of 1 row to the full block
+MANY = {"long": [20011, 0, 9000, 999, 1], "medium": [(37 * i) % 181 for i in range(96)]}
+
+
+@pytest.mark.parametrize("out", DT)
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("K,M", [(16, 1040), (144, 1552), (256, 528), (272, 2048), (400, 1296),
+                                 (512, 272), (656, 1040), (784, 1024), (1008, 784)])
+@pytest.mark.parametrize("counts", list(MANY))
+def test_matmul_i8_many_rows(counts, K, M, swiglu, out):
+    torch = _torch()
+    counts = MANY[counts]
+    E, n = len(counts), sum(counts) + 2
+    x, xs, w, ws = i8_case(n, K, M, E, K + M)
+    offsets = torch.tensor([1] + counts, dtype=torch.int32).cumsum(0).to(torch.int32).cuda()
+    y = torch.full((n, M // 2 if swiglu else M), 7.5, dtype=types()[out], device="cuda")
+    binding.matmul_i8(x, xs, w, ws, offsets=offsets, swiglu=swiglu, y=y)
+    lo = 1
+    for e, c in enumerate(counts):
+        if c:
+            i8_check(y, x, xs, w, ws, lo, lo + c, e, swiglu, (K, M, e))
+        lo += c
+    assert bool((y[0] == 7.5).all()) and bool((y[lo:] == 7.5).all())
+
+
+@pytest.mark.parametrize("out", DT)
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("n,K,M", [(1000, 144, 4112), (700, 272, 4096), (513, 400, 8208),
+                                   (2100, 656, 4112), (30001, 144, 1040), (20480, 272, 2064),
+                                   (16001, 1008, 1040), (9999, 128, 4096)])
+def test_matmul_i8_dense_many_rows(n, K, M, swiglu, out):
+    x, xs, w, ws = i8_case(n, K, M, 1, n)
+    y = binding.matmul_i8(x, xs, w, ws, swiglu=swiglu, dtype=types()[out])
+    i8_check(y, x, xs, w, ws, 0, n, 0, swiglu, (n, K, M))
+
+
 @pytest.mark.parametrize("T,E,K,M,swiglu", [(1, 256, 512, 256, True), (4, 256, 2048, 1024, True),
                                             (32, 256, 512, 2048, False), (192, 255, 256, 512, True),
                                             (300, 60, 1024, 272, False), (1030, 16, 512, 1024, True),
