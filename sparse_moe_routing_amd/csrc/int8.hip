@@ -741,15 +741,15 @@ double likely_tiles(const I8Params &p, int per, double more) {
 
 // Which kernel, and how it is cut, from estimates of all in us. The constants are rates measured on
 // MI355X. Stream waves take their weights and rows in at 8.5 TB/s in all, with a start and end worth
-// 3 KB each. HBM gives 6.4 TB/s to them, 6.1 to the deep block form and 5.2 to the wide one, and an
-// expert's weights are read once per tile. A slab of a block costs 0.33 us and 5.5 ns a row, at
-// least 0.78 (deep) or 1.2 (wide); a unit's end 2 us and its results' stores.
-// Measured where the choice turns (us; the better of 16- and 32-row waves, deep, wide): 256 experts
-// of 2048 x 1024 with SwiGLU, even routing, 6 rows an expert: 82, 88, 97; 12 rows: 91, 90, 99; 31
-// rows: 149, 94, 110; 94 rows: deep 117, wide 124; 144 rows: 199, 140. The same with skewed routing,
-// where hot experts have many tiles: 46, 45, 54; 68, 48, 62; 120, 66, 89; 111, 125; 152, 148. Dense
-// 4096 x 4096, 128 rows: 16, 27, 41; 256 rows: 30, 27, 42; 2048 rows: deep 41, wide 48; 4096 rows:
-// 76, 64.
+// 3 KB each. HBM gives 6.4 TB/s to those of 16 rows, 6.1 to those of 32 and to the deep block form,
+// 5.2 to the wide one, and an expert's weights are read once per tile. A slab of a block costs 0.33 us and 5.5 ns a row, at
+// least 0.78 (deep) or 1.2 (wide); a unit's end 3 or 2 us and its results' stores.
+// Measured where the choice turns (us; 16-row waves, 32-row waves, deep, wide): 256 experts of 2048 x
+// 1024 with SwiGLU, even routing, 6 rows an expert: 83, 85, 87, 97; 8 rows: 84, 88, 89, 99; 12 rows:
+// 96, 91, 90, 99; 31 rows: 184, 149, 94, 110; 94 rows: deep 115, wide 124; 144 rows: 199, 140. The same
+// with skewed routing, where hot experts have many tiles: 49, 47, 44, 54; 57, 55, 45, 55; 75, 68, 48,
+// 64; 142, 120, 67, 91; 112, 125; 153, 149. Dense 4096 x 4096, 128 rows: 27, 16, 27, 41; 256 rows: 47,
+// 31, 27, 42; 2048 rows: deep 41, wide 48; 4096 rows: 76, 64.
 struct Choice {
     bool block;
     int row_tiles, k_split, tile_rows;  // stream: 16-row tiles per wave, waves per block; block: rows
@@ -768,7 +768,8 @@ Choice choose(const I8Params &p, bool swiglu, int out_bytes, int cus) {
     for (int r = p.offsets ? kDeepRows : 64; r <= kBRows; r += p.offsets ? kBRows - kDeepRows : 64) {
         const bool deep = r <= kDeepRows;
         const double tiles = likely_tiles(p, r, 0.35), n = least(rows, r);
-        const double unit = nslab * most(deep ? 0.78 : 1.2, 0.33 + 0.0055 * n) + 2.0 + n * cols * out_bytes / 22e3;
+        const double unit = nslab * most(deep ? 0.78 : 1.2, 0.33 + 0.0055 * n) + (deep ? 3.0 : 2.0) +
+                            n * cols * out_bytes / 22e3;
         const double reads = (p.offsets ? tiles : 1.0) * weights + others;
         const double us = most(ceil(tiles * S / cus) * unit, reads / (deep ? 6.1e6 : 5.2e6));
         if (best == 0 || us <= best) best = us, c.tile_rows = r;
@@ -779,7 +780,7 @@ Choice choose(const I8Params &p, bool swiglu, int out_bytes, int cus) {
         // fewer waves than CUs: their K is split four ways
         const int split = waves <= cus ? 4 : 1;
         const double us = most(waves * ((kSCh + least(rows, nb * kTile)) * p.K + 3000) / 8.5e6,
-                               most(experts * weights / 6.4e6, 0.35 * nslab / split));
+                               most((experts * weights + others) / (nb == 1 ? 6.4e6 : 6.1e6), 0.35 * nslab / split));
         if (us < best) best = us, c.block = false, c.row_tiles = nb, c.k_split = split;
     }
     return c;
