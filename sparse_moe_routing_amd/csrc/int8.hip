@@ -108,9 +108,9 @@ __device__ __forceinline__ void scaled(const i32x4_t &acc, float sx, const float
 }
 
 // ------------------------------------------------------------------------- large row counts
-// The wide form: a block multiplies up to 320 rows of one expert by 256 weight channels (with SwiGLU: 128 gate
-// channels and the 128 up channels that go with them). K is staged in slabs of 128 bytes per row,
-// whole cache lines loaded straight into LDS (buffer loads with the LDS flag: no registers held
+// The wide form: a block multiplies up to 320 rows of one expert by 256 weight channels (with
+// SwiGLU: 128 gate channels and the 128 up channels that go with them). K is staged in slabs of 128
+// bytes per row, whole cache lines loaded straight into LDS (buffer loads with the LDS flag: no registers held
 // while in flight), double-buffered: the next slab's loads are in flight during the current slab's
 // matrix instructions. Eight waves, two per SIMD: wave w takes the channels of half w % 2 and a
 // quarter of the tile's 16-row subtiles, at most five, so that a tile of n rows costs ceil(n / 64)
@@ -129,9 +129,9 @@ __device__ __forceinline__ void scaled(const i32x4_t &acc, float sx, const float
 // Why these sizes: per slab a CU moves 72 KB into LDS and reads 208 KB of operands for 640 matrix
 // instructions; 320 x 256 is the patch with the least LDS traffic per product whose sums still fit
 // two waves' registers, and at 65536 rows of 256 experts most experts' rows fit one tile, so that
-// their weights cross HBM once. Measured: 65536 rows of 256 experts of 2048 x 1024 with SwiGLU 178 us
-// (1.5 Pop/s; 643 MiB read, the least there is; matrix units busy 36 %, waits for operands 38 %);
-// dense 8192 x 4096 x 4096 131 us (2.1 Pop/s). 256-row tiles take 252 us where these take 229 (before
+// their weights cross HBM once. Measured: 65536 rows of 256 experts of 2048 x 1024 with SwiGLU 173 us
+// (1.6 Pop/s; 644 MiB read, the least there is; matrix units busy 39 %, waits 39 %); dense 8192 x 4096
+// x 4096 126 us (2.2 Pop/s). 256-row tiles take 252 us where these take 229 (before
 // the last steps), 128-channel blocks 260, four waves of 128 x 128 318.
 //
 // With fewer rows per expert a slab's matrix work is over long before the next slab has landed, and
@@ -189,8 +189,8 @@ __device__ __forceinline__ void wave_exchange() {
 
 template <bool kSwiglu, class O, bool kOnce, bool kDeep>
 struct BlockProduct {
-    static constexpr int kXSegs = (kDeep ? kDeepRows : kBRows) * kSlabB / 1024 / kBWaves;  // 1 KB row segments
-                                                                                           // per wave
+    // 1 KB row segments per wave (5, deep: 2)
+    static constexpr int kXSegs = (kDeep ? kDeepRows : kBRows) * kSlabB / 1024 / kBWaves;
     static constexpr int kCols = kSwiglu ? kBCh / 2 : kBCh;  // output channels of a block
     static constexpr int kAux = kOnce ? kBufNT : 0;          // cache policy of the weights
     const I8Params &p;
@@ -258,8 +258,8 @@ struct BlockProduct {
         }
     }
     // A block barrier that leaves loads in flight. kRead: after this wave's LDS reads have returned
-    // (what they read may be overwritten); kLoads: after its loads have landed in LDS.
-    // kYoung: all but this many of them.
+    // (what they read may be overwritten); kLoads: after its loads, all but the youngest kYoung, have
+    // landed in LDS.
     template <bool kRead, bool kLoads, int kYoung = 0>
     __device__ __forceinline__ void phase_end() const {
         static_assert(kYoung < 16, "the counter's low bits");
@@ -399,9 +399,9 @@ struct BlockProduct {
             if (wave >= kBWaves / 2) slabs(std::true_type{});
             else slabs(std::false_type{});
         }
-        // Results: the second weight buffer is free now, the next unit's first slab has landed. A wave turns
-        // 16 rows at a time in its 4 KB of it, so that rows leave in whole 16-byte pieces, 256
-        // bytes of a row side by side; pieces rotate by the row (no bank conflicts).
+        // Results: the last weight buffer is free now, the next unit's first slab has landed. A wave
+        // turns 16 rows at a time in its 4 KB of that buffer, so that rows leave in whole 16-byte
+        // pieces, 256 bytes of a row side by side; pieces rotate by the row (no bank conflicts).
         if (busy) {
             constexpr int kOut = kSwiglu ? kBA / 2 : kBA;                  // output subtiles per wave
             constexpr int kPart = 4096 / (kTile * (int)sizeof(O)) / kTile; // subtiles per turn of 4 KB
@@ -447,7 +447,7 @@ struct BlockProduct {
                 }
             }
         }
-        phase_end<true, false>();  // the second buffers may be filled again
+        phase_end<true, false>();  // the last buffers may be filled again
     }
 };
 
