@@ -277,9 +277,9 @@ class MoeLayer:
 # contiguous and on one device; what is not raises ValueError before anything is enqueued, and a
 # call that the library refuses raises MoeError. Without `stream` the work is enqueued on the
 # current stream of the tensors' device; with it, results are allocated for that stream, and the
-# caller orders it after whatever writes the inputs. A decode round's operators take a few
-# microseconds each, so this side is kept short: no Stream object (three microseconds) is made
-# where nothing has to be switched.
+# caller orders it after whatever writes the inputs and keeps them until the work has run. A decode
+# round's operators take a few microseconds each, so this side is kept short: no Stream object
+# (three microseconds) is made where nothing has to be switched.
 _row_types = {}  # torch dtype -> the library's number (filled on first use)
 
 
