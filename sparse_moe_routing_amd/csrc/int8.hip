@@ -635,6 +635,7 @@ __global__ __launch_bounds__(kKS *kWave) void i8_stream_kernel(I8Params p) {
         auto turn = [&](auto ic, int i) __attribute__((always_inline)) {
             constexpr int B = decltype(ic)::value;
             __builtin_amdgcn_s_waitcnt(kWait);
+            __builtin_amdgcn_sched_barrier(0);  // the loads counted above stay on their side of it
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint4 a[2];
@@ -645,6 +646,11 @@ __global__ __launch_bounds__(kKS *kWave) void i8_stream_kernel(I8Params p) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) mma_i8(acc[k][j], a[k], xr[B][j][h]);
             }
+            // The refill goes into the slot that was read: it is requested once the reads have returned
+            // (one past K is answered without a memory access, so latency orders nothing).
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // LDS reads: none outstanding; loads: not waited for
+            __builtin_amdgcn_sched_barrier(0);
             const bool here = i + kRing < turns;  // uniform
             issue(ic, here ? cur : nxt, here ? i + kRing : i + kRing - turns, here || more);
         };
