@@ -523,7 +523,8 @@ __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(
 // takes the next unit's first slabs while the last slabs and the results of the present one are
 // worked on, so that the stream does not stop between them.
 // kKS waves make a block and split K between them (their integer sums join in LDS, exact in any
-// order) where there is so little to stream that single waves would not cover the chip.
+// order) where there is so little to stream that single waves would not cover the chip; each such
+// block takes one unit.
 // Measured: 256 rows over 256 experts of 2048 x 1024 with SwiGLU 53 us (6.3 TB/s of weights; plain
 // instead of non-temporal loads 63, slabs of half cache lines 65 and more); one row of 4096 x 4096 6
 // us.
@@ -538,6 +539,7 @@ __global__ __launch_bounds__(kKS *kWave) void i8_stream_kernel(I8Params p) {
         ring2[kKS][kSlabBytes], ring3[kKS][kSlabBytes];
     constexpr int kCols = kSwiglu ? kSCh / 2 : kSCh;  // output channels of a block
     constexpr int kRows = kTile * kNB;
+    constexpr bool kWalk = kKS == 1;
     const int lane = lane_id(), wave = kKS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
     const int col = lane & 15, q = lane >> 4;
     auto slot = [&](auto ic) __attribute__((always_inline)) -> unsigned char * {
@@ -614,7 +616,7 @@ __global__ __launch_bounds__(kKS *kWave) void i8_stream_kernel(I8Params p) {
     issue(I3{}, cur, 3, true);
     for (;;) {
         u += step;
-        const bool more = u < last;
+        const bool more = kWalk && u < last;
         const Unit nxt = more ? unit(u) : cur;
         // the unit's scales, requested before its products: rows and channels past it read as zero
         // (their results are not stored)
@@ -682,7 +684,6 @@ __global__ __launch_bounds__(kKS *kWave) void i8_stream_kernel(I8Params p) {
                         for (int j = 0; j < kNB; ++j)
                             acc[k][j] += *reinterpret_cast<const i32x4_t *>(red[w][k][j][lane]);
             }
-            if (more) __syncthreads();  // uniform: the sums are read before the next unit's are written
         }
         if (mine) {
 #pragma unroll
@@ -823,9 +824,10 @@ hipError_t launch_matmul_i8(const I8Params &p, bool swiglu, int y_dtype, hipStre
     const long units = most_tiles(p, c.row_tiles * kTile) * ((Mo + cols - 1) / cols);
     // a wave walks units of about 64 KB of weights in all: shorter walks pay their starts too often
     // (512 x 2048, 2 rows an expert: 45 us for one unit a wave, 39 for four), longer ones even out
-    // badly at the end (42 for eight); more only while the chip has no room for more waves
+    // badly at the end (42 for eight); more only while the chip has no room for more waves. With K split
+    // a block per unit: choose() splits only where there are at most twice as many as CUs
     const long walk = p.K < 2048 ? 2048 / p.K : 1, room = (long)cus * kStreamBlocks;
-    const long blocks = units <= room ? units : (units + walk - 1) / walk > room ? (units + walk - 1) / walk : room;
+    const long blocks = units <= room || c.k_split > 1 ? units : (units + walk - 1) / walk > room ? (units + walk - 1) / walk : room;
     const unsigned grid = (unsigned)((blocks + kXcds - 1) / kXcds * kXcds);
     typed([&](auto o, auto glu) {
         using O = decltype(o);

@@ -114,3 +114,11 @@ def test_the_scan_sees_an_early_refill():
     assert [line for _, _, line in early] == ["buffer_load_dwordx4 v8, s[0:3], 0 offen lds"]
     del listing[7]
     assert refills_before_reads(listing) == []
+
+
+def test_split_blocks_take_one_unit(kernels):
+    """Where the waves of a block split K there are no more units than blocks: the waves meet once,
+    to join their sums, and no loop carries them on to another unit."""
+    split = {name: lines for name, lines in kernels.items() if re.search(r"stream.*Li4EEEv", name)}
+    assert len(split) == 8
+    assert {sum(line == "s_barrier" for line in lines) for lines in split.values()} == {1}
