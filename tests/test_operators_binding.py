@@ -1,0 +1,247 @@
+"""The binding's checks of the separate operators, argument by argument: a good call with one operand
+changed raises ValueError with the message of that check, and the library is not called. The
+same table runs on the CPU, with the library and the device lookup stood in for, and on the GPU
+as users call it."""
+import pytest
+
+from sparse_moe_routing_amd import binding
+
+T, H, N, E, M, K = 4, 64, 32, 2, 48, 64
+
+
+def good(device):
+    """(function, its good operands) of every operator."""
+    import torch
+
+    def f32(*shape):
+        return torch.zeros(shape, device=device)
+
+    def i8(*shape):
+        return torch.zeros(shape, dtype=torch.int8, device=device)
+
+    def rows():
+        return torch.arange(N, dtype=torch.int32, device=device)
+
+    def offsets():
+        return torch.tensor([0, 3, 9], dtype=torch.int32, device=device)
+
+    return {
+        "permute": (binding.permute, dict(x=f32(T, H), rows=rows(), n_rows=N, xs=f32(N, H))),
+        "permute_backward": (binding.permute_backward, dict(dxs=f32(N, H), rows=rows(),
+                                                            dx=f32(T, H))),
+        "unpermute": (binding.unpermute, dict(ys=f32(N, H), rows=rows(), w=f32(T, 8),
+                                              shared=f32(T, H), gate=f32(T), y=f32(T, H))),
+        "unpermute_backward": (binding.unpermute_backward,
+                               dict(dy=f32(T, H), ys=f32(N, H), rows=rows(), w=f32(T, 8),
+                                    shared=f32(T, H), gate=f32(T), dys=f32(N, H))),
+        "quantize_i8": (binding.quantize_i8, dict(x=f32(T, H))),
+        "permute_i8": (binding.permute_i8, dict(x=f32(T, H), rows=rows(), n_rows=N)),
+        "matmul_i8": (binding.matmul_i8, dict(x=i8(9, K), x_scale=f32(9), w=i8(E, M, K),
+                                              w_scale=f32(E, M), offsets=offsets(), y=f32(9, M))),
+    }
+
+
+def shorter(t):
+    return t[1:].contiguous()
+
+
+def narrower(t):
+    return t[..., 8:].contiguous()
+
+
+def strided(t):
+    import torch
+    return torch.stack([t, t], dim=-1)[..., 0]
+
+
+def half(t):
+    return t.half()
+
+
+def long(t):
+    return t.long()
+
+
+def double(t):
+    return t.double()
+
+
+def none(t):
+    return None
+
+
+# operator, operand, change, the check's message
+REFUSED = [
+    ("permute", "x", half, "x: dtype"), ("permute", "x", strided, "x must be contiguous"),
+    ("permute", "x", lambda t: t[None], "values to unpack"),
+    ("permute", "x", shorter, "rows: shape"), ("permute", "x", narrower, "xs: shape"),
+    ("permute", "rows", long, "rows: dtype"), ("permute", "rows", shorter, "rows: shape"),
+    ("permute", "rows", lambda t: t.reshape(T, 8), "rows: shape"),
+    ("permute", "rows", strided, "rows must be contiguous"),
+    ("permute", "n_rows", lambda n: n + 1, "xs: shape"),
+    ("permute", "xs", half, "xs: dtype"), ("permute", "xs", shorter, "xs: shape"),
+    ("permute", "xs", narrower, "xs: shape"), ("permute", "xs", strided, "xs must be contiguous"),
+    ("permute_backward", "dxs", half, "dxs: dtype"),
+    ("permute_backward", "dxs", strided, "dxs must be contiguous"),
+    ("permute_backward", "dxs", narrower, "dx: shape"),
+    ("permute_backward", "rows", long, "rows: dtype"),
+    ("permute_backward", "rows", shorter, "rows: shape"),
+    ("permute_backward", "dx", half, "dx: dtype"), ("permute_backward", "dx", shorter, "dx: shape"),
+    ("permute_backward", "dx", strided, "dx must be contiguous"),
+    ("unpermute", "ys", half, "ys: dtype"), ("unpermute", "ys", strided, "ys must be contiguous"),
+    ("unpermute", "ys", narrower, "shared: shape"),
+    ("unpermute", "rows", long, "rows: dtype"), ("unpermute", "rows", shorter, "rows: shape"),
+    ("unpermute", "w", double, "w: dtype"), ("unpermute", "w", shorter, "rows: shape"),
+    ("unpermute", "w", lambda t: t[:, :7].contiguous(), "w: shape"),
+    ("unpermute", "w", strided, "w must be contiguous"),
+    ("unpermute", "shared", none, "both or neither"), ("unpermute", "gate", none, "both or neither"),
+    ("unpermute", "shared", half, "shared: dtype"), ("unpermute", "shared", shorter, "shared: shape"),
+    ("unpermute", "shared", strided, "shared must be contiguous"),
+    ("unpermute", "gate", double, "gate: dtype"), ("unpermute", "gate", shorter, "gate: shape"),
+    ("unpermute", "gate", strided, "gate must be contiguous"),
+    ("unpermute", "dtype", lambda _: binding_dtype("bfloat16"), "y: dtype"),
+    ("unpermute", "y", half, "y: dtype"), ("unpermute", "y", shorter, "y: shape"),
+    ("unpermute", "y", strided, "y must be contiguous"),
+    ("unpermute_backward", "dy", half, "dy: dtype"),
+    ("unpermute_backward", "dy", shorter, "dy: shape"),
+    ("unpermute_backward", "dy", narrower, "dy: shape"),
+    ("unpermute_backward", "dy", strided, "dy must be contiguous"),
+    ("unpermute_backward", "ys", half, "ys: dtype"),
+    ("unpermute_backward", "ys", narrower, "dy: shape"),
+    ("unpermute_backward", "ys", strided, "ys must be contiguous"),
+    ("unpermute_backward", "rows", long, "rows: dtype"),
+    ("unpermute_backward", "rows", shorter, "rows: shape"),
+    ("unpermute_backward", "w", double, "w: dtype"),
+    ("unpermute_backward", "w", shorter, "dy: shape"),
+    ("unpermute_backward", "shared", none, "both or neither"),
+    ("unpermute_backward", "gate", none, "both or neither"),
+    ("unpermute_backward", "shared", shorter, "shared: shape"),
+    ("unpermute_backward", "gate", shorter, "gate: shape"),
+    ("unpermute_backward", "dys", half, "dys: dtype"),
+    ("unpermute_backward", "dys", shorter, "dys: shape"),
+    ("unpermute_backward", "dys", strided, "dys must be contiguous"),
+    ("quantize_i8", "x", half, "x: dtype"), ("quantize_i8", "x", strided, "x must be contiguous"),
+    ("quantize_i8", "x", lambda t: t[0], "values to unpack"),
+    ("permute_i8", "x", half, "x: dtype"), ("permute_i8", "x", strided, "x must be contiguous"),
+    ("permute_i8", "x", shorter, "rows: shape"), ("permute_i8", "rows", long, "rows: dtype"),
+    ("permute_i8", "rows", shorter, "rows: shape"),
+    ("matmul_i8", "x", long, "x: dtype"), ("matmul_i8", "x", strided, "x must be contiguous"),
+    ("matmul_i8", "x", narrower, "w: shape"), ("matmul_i8", "x", shorter, "x_scale: shape"),
+    ("matmul_i8", "x_scale", double, "x_scale: dtype"),
+    ("matmul_i8", "x_scale", shorter, "x_scale: shape"),
+    ("matmul_i8", "x_scale", strided, "x_scale must be contiguous"),
+    ("matmul_i8", "w", long, "w: dtype"), ("matmul_i8", "w", strided, "w must be contiguous"),
+    ("matmul_i8", "w", lambda t: t[0], "values to unpack"),
+    ("matmul_i8", "w", shorter, "w_scale: shape"),
+    ("matmul_i8", "w_scale", double, "w_scale: dtype"),
+    ("matmul_i8", "w_scale", narrower, "w_scale: shape"),
+    ("matmul_i8", "w_scale", shorter, "w_scale: shape"),
+    ("matmul_i8", "w_scale", strided, "w_scale must be contiguous"),
+    ("matmul_i8", "offsets", long, "offsets: dtype"),
+    ("matmul_i8", "offsets", shorter, "offsets: shape"),
+    ("matmul_i8", "offsets", strided, "offsets must be contiguous"),
+    ("matmul_i8", "swiglu", lambda _: True, "y: shape"),
+    ("matmul_i8", "dtype", lambda _: binding_dtype("bfloat16"), "y: dtype"),
+    ("matmul_i8", "y", half, "y: dtype"), ("matmul_i8", "y", shorter, "y: shape"),
+    ("matmul_i8", "y", narrower, "y: shape"), ("matmul_i8", "y", strided, "y must be contiguous"),
+]
+IDS = [f"{op}-{arg}-{i}" for i, (op, arg, _, _) in enumerate(REFUSED)]
+OPERATORS = ("permute", "permute_backward", "unpermute", "unpermute_backward", "quantize_i8",
+             "permute_i8", "matmul_i8")
+
+
+def binding_dtype(name):
+    import torch
+    return getattr(torch, name)
+
+
+def refuse(device, op, arg, change, message):
+    f, operands = good(device)[op]
+    operands[arg] = change(operands.get(arg))
+    with pytest.raises(ValueError, match=message):
+        f(**operands)
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Calls that reach the library, as [(entry point, arguments)], with CPU tensors taken for a
+    device's: their device number is -1 where a GPU's is its index."""
+    import torch
+    seen = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: seen.append((name, args)) or binding.MOE_OK
+
+    want = binding._want
+    monkeypatch.setattr(binding, "_want", lambda name, t, dtype, shape, at: want(name, t, dtype, shape, -1))
+    monkeypatch.setattr(binding, "_switched", lambda device, stream: None)
+    monkeypatch.setattr(binding, "load", lambda: Library())
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0, raising=False)
+    return seen
+
+
+@pytest.mark.parametrize("op", OPERATORS)
+def test_good_call_reaches_the_library(calls, op):
+    """What the refusals change is all that is wrong with them; addresses go in as given."""
+    f, operands = good("cpu")[op]
+    f(**operands)
+    assert [name for name, _ in calls] == ["moe_" + op]
+    given = [v.data_ptr() for v in operands.values() if hasattr(v, "data_ptr")]
+    assert set(given) <= set(calls[0][1])
+
+
+@pytest.mark.parametrize("op,arg,change,message", REFUSED, ids=IDS)
+def test_refused(calls, op, arg, change, message):
+    refuse("cpu", op, arg, change, message)
+    assert calls == []
+
+
+@pytest.mark.parametrize("op", OPERATORS)
+def test_refused_off_the_gpu(op):
+    f, operands = good("cpu")[op]
+    with pytest.raises(ValueError, match="tensors must be on a GPU, not on cpu"):
+        f(**operands)
+
+
+def needs_gpu():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("op,arg,change,message", REFUSED, ids=IDS)
+def test_refused_on_the_gpu(op, arg, change, message):
+    needs_gpu()
+    refuse("cuda", op, arg, change, message)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("op", OPERATORS)
+def test_operand_elsewhere_refused(op):
+    """Every operand but the first, which says where the call runs, left in host memory."""
+    needs_gpu()
+    f, operands = good("cuda")[op]
+    names = [a for a, v in operands.items() if hasattr(v, "cpu")]
+    first = "ys" if "ys" in names else names[0]
+    for a in names:
+        if a != first:
+            with pytest.raises(ValueError, match=f"{a} is on cpu, expected cuda:0"):
+                f(**dict(operands, **{a: operands[a].cpu()}))
+    f(**operands)
+
+
+@pytest.mark.gpu
+def test_misaligned_rows_refused():
+    """Contiguous views that begin off a 16-byte boundary are the library's to refuse."""
+    torch = needs_gpu()
+    room = torch.zeros(N * H + 1, device="cuda")
+    for op, arg, shape in (("permute", "x", (T, H)), ("permute", "xs", (N, H)),
+                           ("unpermute", "ys", (N, H)), ("quantize_i8", "x", (T, H))):
+        f, operands = good("cuda")[op]
+        operands[arg] = room[1:1 + shape[0] * shape[1]].view(shape)
+        with pytest.raises(binding.MoeError) as e:
+            f(**operands)
+        assert e.value.status == binding.MOE_ERR_INVALID_ARG
