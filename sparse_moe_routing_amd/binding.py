@@ -179,6 +179,14 @@ class MoeLayer:
         import torch
         return torch.zeros(max(self.workspace_bytes(T), 256), dtype=torch.uint8, device=device)
 
+    def _zeroed(self, T, device, stream):
+        """A workspace of one call: allocated for and zeroed on the stream that the call runs on
+        (zeroed on another one it could still hold old counters when the kernels start, and be
+        given away while they run)."""
+        import torch
+        with torch.cuda.stream(stream):
+            return self.workspace(T, device)
+
     def route(self, x=None, logits=None, T=None, ws=None, want_logits=True, stream=None):
         """(logits [T][R] or None, ids [T][8], w [T][8], g [T] or None) from x or given logits."""
         import torch
@@ -189,7 +197,7 @@ class MoeLayer:
         w = torch.empty((T, 8), dtype=torch.float32, device=dev)
         g = torch.empty((T,), dtype=torch.float32, device=dev) if self.shared_inter > 0 else None
         z = torch.empty((T, self.rows), dtype=torch.float32, device=dev) if want_logits else None
-        ws = self.workspace(T, dev) if ws is None else ws
+        ws = self._zeroed(T, dev, stream) if ws is None else ws
         _check(self.lib.moe_route(self.ctx, _ptr(x), _ptr(logits), T, _ptr(z), _ptr(ids),
                                   _ptr(w), _ptr(g), _ptr(ws), ws.numel(), _stream(stream)),
                "moe_route")
@@ -203,7 +211,7 @@ class MoeLayer:
         counts = torch.empty((self.num_experts,), dtype=torch.int32, device=dev)
         offsets = torch.empty((self.num_experts + 1,), dtype=torch.int32, device=dev)
         perm = torch.empty((T * 8,), dtype=torch.int32, device=dev)
-        ws = self.workspace(T, dev) if ws is None else ws
+        ws = self._zeroed(T, dev, stream) if ws is None else ws
         _check(self.lib.moe_bucket(self.ctx, _ptr(ids), T, _ptr(counts), _ptr(offsets),
                                    _ptr(perm), _ptr(ws), ws.numel(), _stream(stream)),
                "moe_bucket")
@@ -223,7 +231,7 @@ class MoeLayer:
             with torch.cuda.stream(stream):
                 counts.zero_()
                 offsets.zero_()
-        ws = self.workspace(T, dev) if ws is None else ws
+        ws = self._zeroed(T, dev, stream) if ws is None else ws
         _check(self.lib.moe_bucket_rows(self.ctx, _ptr(ids), T, _ptr(counts), _ptr(offsets),
                                         _ptr(perm), _ptr(rows), _ptr(ws), ws.numel(),
                                         _stream(stream)), "moe_bucket_rows")
@@ -235,7 +243,7 @@ class MoeLayer:
         T = x.shape[0]
         dev = x.device
         y = torch.empty((T, self.hidden), dtype=torch.float32, device=dev) if y is None else y
-        ws = self.workspace(T, dev) if ws is None else ws
+        ws = self._zeroed(T, dev, stream) if ws is None else ws
         ids = w = g = None
         if routing is not None:
             ids, w, g = routing

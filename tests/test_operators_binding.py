@@ -245,3 +245,94 @@ def test_misaligned_rows_refused():
         with pytest.raises(binding.MoeError) as e:
             f(**operands)
         assert e.value.status == binding.MOE_ERR_INVALID_ARG
+
+
+# ----------------------------------------------------------------------------- the layer's calls
+@pytest.fixture
+def layer(monkeypatch):
+    """A MoeLayer without a device: its library answers every call with success and writes (entry
+    point, arguments) down, next to the stream that each zeroed allocation was made on."""
+    import contextlib
+
+    import torch
+    m = binding.MoeLayer.__new__(binding.MoeLayer)
+    m.ctx, m.num_experts, m.shared_inter, m.rows, m.hidden = None, 16, 0, 16, 64
+    m.seen, now = [], [None]
+
+    class Library:
+        def moe_workspace_bytes(self, ctx, tokens):
+            return 512
+
+        def __getattr__(self, name):
+            return lambda *args: m.seen.append((name, args)) or binding.MOE_OK
+
+    m.lib = Library()
+    zeros = torch.zeros
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, now[0] = now[0], stream if stream is not None else now[0]
+        yield
+        now[0] = before
+
+    def noted(*args, **kwargs):
+        m.seen.append(("zeros", now[0]))
+        return zeros(*args, **kwargs)
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch, "zeros", noted)
+    monkeypatch.setattr(binding, "_stream", lambda stream=None: stream)
+    return m
+
+
+LAYER_CALLS = {
+    "route": lambda m, x, ids, **k: m.route(x=x, **k),
+    "bucket": lambda m, x, ids, **k: m.bucket(ids, **k),
+    "bucket_rows": lambda m, x, ids, **k: m.bucket_rows(ids, **k),
+    "forward": lambda m, x, ids, **k: m.forward(x, **k),
+}
+
+
+@pytest.mark.parametrize("name", list(LAYER_CALLS))
+def test_workspace_is_zeroed_on_the_calls_stream(layer, name):
+    """Without a workspace of the caller's the call zeroes one: on the stream that its kernels are
+    enqueued on, or nothing orders the fill before them."""
+    import torch
+    x, ids = torch.ones(4, 64), torch.ones((4, 8), dtype=torch.int32)
+    for stream in (None, "side"):
+        layer.seen.clear()
+        LAYER_CALLS[name](layer, x, ids, stream=stream)
+        assert layer.seen[0] == ("zeros", stream)
+        assert layer.seen[1][0] == "moe_" + name and stream in layer.seen[1][1]
+        assert len(layer.seen) == 2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", list(LAYER_CALLS))
+def test_layer_call_on_a_side_stream(name):
+    """The same results on a side stream while the current one is busy and its freed memory holds
+    other values."""
+    torch = needs_gpu()
+    from sparse_moe_routing_amd import inputs
+    m, t = binding.layer_from_numpy(inputs.make_layer(inputs.BY_NAME["tiny_fp32_t4"]), 64)
+    ids = m.route(x=t["x"])[1]
+
+    def results(stream=None):
+        out = LAYER_CALLS[name](m, t["x"], ids, stream=stream)
+        return [v for v in (out if isinstance(out, tuple) else (out,)) if v is not None]
+
+    want = results()
+    side = torch.cuda.Stream()
+    busy = torch.ones(1 << 26, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(3):
+        # what the current stream's allocator hands out next holds ones
+        torch.full((m.workspace_bytes(64),), 1, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        for _ in range(8):
+            busy.mul_(1.0)
+        got = results(side)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    torch.cuda.synchronize()
+    m.close()
