@@ -219,22 +219,27 @@ class MoeLayer:
 
     def bucket_rows(self, ids, ws=None, stream=None):
         """(counts [E], offsets [E+1], perm [T*8], rows [T*8]): bucket() and the inverse of perm,
-        the table that the row operators below take (-1: the pair's id is outside [0, E))."""
+        the table that the row operators below take (-1: the pair's id is outside [0, E)). ids,
+        device and stream are checked and used as by those operators."""
         import torch
-        T = ids.shape[0]
         dev = ids.device
+        ctx = _switched(dev, stream)
+        if ctx is not None:
+            with ctx:
+                return self.bucket_rows(ids, ws)
+        T = ids.shape[0]
+        at = _want("ids", ids, torch.int32, (T, 8), dev.index)
         counts = torch.empty((self.num_experts,), dtype=torch.int32, device=dev)
         offsets = torch.empty((self.num_experts + 1,), dtype=torch.int32, device=dev)
         perm = torch.empty((T * 8,), dtype=torch.int32, device=dev)
         rows = torch.empty((T * 8,), dtype=torch.int32, device=dev)
         if T == 0:  # the library enqueues nothing: no pairs
-            with torch.cuda.stream(stream):
-                counts.zero_()
-                offsets.zero_()
-        ws = self._zeroed(T, dev, stream) if ws is None else ws
-        _check(self.lib.moe_bucket_rows(self.ctx, _ptr(ids), T, _ptr(counts), _ptr(offsets),
-                                        _ptr(perm), _ptr(rows), _ptr(ws), ws.numel(),
-                                        _stream(stream)), "moe_bucket_rows")
+            counts.zero_()
+            offsets.zero_()
+        ws = self.workspace(T, dev) if ws is None else ws
+        _check(self.lib.moe_bucket_rows(self.ctx, at, T, _ptr(counts), _ptr(offsets), _ptr(perm),
+                                        _ptr(rows), _ptr(ws), ws.numel(), _stream()),
+               "moe_bucket_rows")
         return counts, offsets, perm, rows
 
     def forward(self, x, routing=None, y=None, ws=None, stream=None, events=None):
