@@ -292,7 +292,9 @@ class MoeLayer:
 # current stream of the tensors' device; with it, results are allocated for that stream, and the
 # caller orders it after whatever writes the inputs and keeps them until the work has run. A decode
 # round's operators take a few microseconds each, so this side is kept short: no Stream object
-# (three microseconds) is made where nothing has to be switched.
+# (three microseconds) is made where nothing has to be switched. permute and unpermute are recorded by
+# autograd (autograd.py); the others give results without a gradient: 8-bit codes have none, and the
+# gradients' own operators are not differentiated again.
 _row_types = {}  # torch dtype -> the library's number (filled on first use)
 
 
@@ -335,15 +337,29 @@ def _switched(device, stream):
     return None
 
 
+def _recorded(out, name):
+    """For a call whose operands require a gradient: whether one is recorded. A result buffer given
+    by the caller is refused then, as by torch's own operators."""
+    import torch
+    if not torch.is_grad_enabled():
+        return False
+    if out is not None:
+        raise ValueError(f"{name} cannot be given where a gradient is recorded (use torch.no_grad())")
+    return True
+
+
 def permute(x, rows, n_rows=None, xs=None, stream=None):
     """xs [n_rows][H] with xs[rows[8t + k]] = x[t] for x [T][H] (fp32 or bf16); n_rows: by default
-    T * 8, or the rows of xs. Rows that no pair names keep what xs held."""
+    T * 8, or the rows of xs. Rows that no pair names keep what xs held. Differentiable in x."""
     import torch
     dev = x.device
     ctx = _switched(dev, stream)
     if ctx is not None:
         with ctx:
             return permute(x, rows, n_rows, xs)
+    if x.requires_grad and _recorded(xs, "xs"):
+        from .autograd import Permute
+        return Permute.apply(x, rows, n_rows)
     (T, H), dt, at = x.shape, x.dtype, dev.index
     num = _row_enum("x", dt)
     px, pr = _want("x", x, dt, (T, H), at), _want("rows", rows, torch.int32, (T * 8,), at)
@@ -389,13 +405,18 @@ def _weighted(ys, rows, w, shared, gate, at):
 
 def unpermute(ys, rows, w, shared=None, gate=None, dtype=None, y=None, stream=None):
     """y [T][H] with y[t] = sum_k w[t][k] ys[rows[8t + k]] + gate[t] shared[t]; y of `dtype`
-    (by default that of ys)."""
+    (by default that of ys). Differentiable in ys, w, shared and gate; the gradient of a row of ys
+    that no pair names is 0."""
     import torch
     dev = ys.device
     ctx = _switched(dev, stream)
     if ctx is not None:
         with ctx:
             return unpermute(ys, rows, w, shared, gate, dtype, y)
+    if (ys.requires_grad or w.requires_grad or (shared is not None and shared.requires_grad) or
+            (gate is not None and gate.requires_grad)) and _recorded(y, "y"):
+        from .autograd import Unpermute
+        return Unpermute.apply(ys, rows, w, shared, gate, dtype)
     (n, H), T, at = ys.shape, w.shape[0], dev.index
     num = _row_enum("ys", ys.dtype)
     py, pr, pw, ps, pg = _weighted(ys, rows, w, shared, gate, at)

@@ -247,6 +247,74 @@ def test_misaligned_rows_refused():
         assert e.value.status == binding.MOE_ERR_INVALID_ARG
 
 
+# ----------------------------------------------------------------------------- autograd
+def test_permute_records_its_gradient(calls):
+    """A tensor that requires a gradient gets it through the library's gradient operator, on a
+    contiguous, 16-byte aligned copy where autograd's own is neither."""
+    import torch
+    f, a = good("cpu")["permute"]
+    x = a["x"].requires_grad_()
+    xs = f(x, a["rows"])
+    assert xs.requires_grad and [name for name, _ in calls] == ["moe_permute"]
+    xs.sum().backward()  # an expanded gradient
+    assert [name for name, _ in calls] == ["moe_permute", "moe_permute_backward"]
+    address, rows = calls[1][1][:2]
+    assert rows == a["rows"].data_ptr() and address % 16 == 0
+    assert x.grad.shape == x.shape
+    room = torch.zeros(N * H + 1)
+    f(x, a["rows"]).backward(room[1:].view(N, H))  # a view off the boundary
+    assert calls[3][1][0] % 16 == 0
+
+
+@pytest.mark.parametrize("arg", ["ys", "w", "shared", "gate"])
+def test_unpermute_records_its_gradients(calls, arg):
+    f, a = good("cpu")["unpermute"]
+    del a["y"]
+    a[arg].requires_grad_()
+    y = f(**a)
+    assert y.requires_grad and [name for name, _ in calls] == ["moe_unpermute"]
+    y.sum().backward()
+    assert [name for name, _ in calls] == ["moe_unpermute", "moe_unpermute_backward"]
+    assert calls[1][1][1:6] == tuple(a[k].data_ptr() for k in ("ys", "rows", "w", "shared", "gate"))
+    for k in ("ys", "w", "shared", "gate"):
+        assert (a[k].grad is not None) == (k == arg)
+
+
+def test_buffers_and_gradients_exclude_each_other(calls):
+    """A result buffer while a gradient is recorded is refused; without recording it is filled."""
+    import torch
+    for op, arg, out in (("permute", "x", "xs"), ("unpermute", "ys", "y"), ("unpermute", "w", "y"),
+                         ("unpermute", "shared", "y"), ("unpermute", "gate", "y")):
+        f, a = good("cpu")[op]
+        a[arg].requires_grad_()
+        with pytest.raises(ValueError, match=f"{out} cannot be given where a gradient is recorded"):
+            f(**a)
+        assert calls == []
+        with torch.no_grad():
+            assert f(**a) is a[out] and not a[out].requires_grad
+            del a[out]
+            assert not f(**a).requires_grad
+        assert [name for name, _ in calls] == ["moe_" + op] * 2
+        calls.clear()
+
+
+def test_refusals_hold_where_a_gradient_is_recorded(calls):
+    import torch
+    f, a = good("cpu")["permute"]
+    with pytest.raises(ValueError, match="rows: dtype"):
+        f(a["x"].requires_grad_(), a["rows"].long())
+    f, a = good("cpu")["unpermute"]
+    with pytest.raises(ValueError, match="both or neither"):
+        f(a["ys"], a["rows"], a["w"].requires_grad_(), gate=a["gate"])
+    assert calls == []
+    # a second derivative is refused, not dropped
+    f, a = good("cpu")["permute"]
+    x = a["x"].requires_grad_()
+    dx, = torch.autograd.grad(f(x, a["rows"]).square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dx.sum().backward()
+
+
 # ----------------------------------------------------------------------------- the layer's calls
 @pytest.fixture
 def layer(monkeypatch):
