@@ -88,17 +88,42 @@ __device__ __forceinline__ void store4(uint16_t *p, const float (&v)[4]) {
     *reinterpret_cast<uint2 *>(p) = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
 }
 
-// silu(z) = z / (1 + e^-z) in about ten instructions (the epilogue of a gate/up product forms one
-// for every two sums): e^-z = 2^t (1 + c), t the rounded product -z log2(e) and c the part that
-// the rounding and the constant left off, so that the error stays a few steps of fp32 however
-// large z is. The bound on the exponent keeps t and c finite; past it e^-z is 0 or infinite anyway.
+// silu(z) = z / (1 + e^-z). e^-z = 2^t (1 + c), t the rounded product -z log2(e) and c the part that
+// the rounding and the constant left off, so that the error stays a few steps of fp32 however large
+// z is. The bound on the exponent keeps t and c finite.
+constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596299e-8f, kLn2 = 0.693147182f;
+__device__ __forceinline__ float exp_rest(float a, float t) {
+    return fmaf(a, kLog2eRest, fmaf(a, kLog2e, -t)) * kLn2;
+}
+// Gates from kFarGate up: about ten instructions. Below it 1 + e^-z passes 2^126 and its reciprocal,
+// which the hardware gives as 0, is no normal number any more.
+constexpr float kFarGate = -87.0f;
 __device__ __forceinline__ float silu(float z) {
-    constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596299e-8f, kLn2 = 0.693147182f;
     const float a = __builtin_amdgcn_fmed3f(-z, -150.0f, 150.0f);
     const float t = a * kLog2e;
-    const float c = fmaf(a, kLog2eRest, fmaf(a, kLog2e, -t)) * kLn2;
-    const float e = __builtin_amdgcn_exp2f(t) * (1.0f + c);
+    const float e = __builtin_amdgcn_exp2f(t) * (1.0f + exp_rest(a, t));
     return z * __builtin_amdgcn_rcpf(1.0f + e);
+}
+// Gates below kFarGate, where 1 + e^-z is e^-z to far less than a step: z e^z, a normal number down to
+// z = -91.9. e^z is multiplied in by halves, which are normal where the result is not yet 0. (Past
+// -1000 it is 0 whatever z is; -infinity gives NaN, as the quotient above.)
+__device__ __forceinline__ float silu_far(float z) {
+    const float a = fmaxf(z, -1000.0f);
+    const float t = a * kLog2e, h = __builtin_amdgcn_exp2f(0.5f * t);
+    return z * h * (1.0f + exp_rest(a, t)) * h;
+}
+// z = silu(z) up of four channels. Far gates are as good as never met: one test for all four.
+__device__ __forceinline__ void swiglu4(float (&z)[4], const float (&up)[4]) {
+    float s[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s[r] = silu(z[r]);
+    if (__builtin_expect(fminf(fminf(z[0], z[1]), fminf(z[2], z[3])) < kFarGate, 0)) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (z[r] < kFarGate) s[r] = silu_far(z[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) z[r] = s[r] * up[r];
 }
 
 // z = fp32(sum) * x_scale * w_scale of four channels.
@@ -425,8 +450,7 @@ struct BlockProduct {
                         if constexpr (kSwiglu) {
                             float up[4];
                             scaled(acc[kOut + i][j], sx, kDeep ? sws[kOut + i] : sw + (kOut + i) * kTile, up);
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) z[r] = silu(z[r]) * up[r];
+                            swiglu4(z, up);
                         }
                         const int at = ((i - i0) * kTile + 4 * lq) * (int)sizeof(O);
                         store4(reinterpret_cast<O *>(stage + lc * kRowB +
@@ -700,8 +724,7 @@ __global__ __launch_bounds__(kKS *kWave) void i8_stream_kernel(I8Params p) {
                     if constexpr (kSwiglu) {
                         float up[4];
                         scaled(acc[1][j], sx[j], sw[1], up);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) z[r] = silu(z[r]) * up[r];
+                        swiglu4(z, up);
                     }
                     store4(y + mc, z);
                 }
