@@ -250,8 +250,10 @@ int moe_permute_i8(const void *x, const int32_t *rows, int32_t T, int32_t H, int
  * that order in fp32. swiglu == 0: y [n_rows][M] = z; otherwise M = 2I with the gate rows first and
  * y [n_rows][I] = silu(z[n][i]) z[n][I + i]. y is rounded once to `y_dtype`. Rows outside
  * [offsets[0], offsets[E]) are left as they were. offsets are clamped to [0, n_rows]; where they
- * fall, y is unspecified, but nothing outside it is touched. n_rows: 0..8388608; E: 1..256;
- * K: 16..16384, a multiple of 16; M: 8..65536, a multiple of 8 (of 16 with swiglu). */
+ * fall, y is unspecified, but nothing outside it is touched. The kernel is chosen from the sizes, with
+ * n_rows taken as spread evenly over the E experts; every choice gives the same bits. n_rows:
+ * 0..8388608; E: 1..256; K: 16..16384, a multiple of 16; M: 8..65536, a multiple of 8 (of 16 with
+ * swiglu). */
 int moe_matmul_i8(const int8_t *x, const float *x_scale, int32_t n_rows, const int8_t *w,
                   const float *w_scale, int32_t E, int32_t M, int32_t K, const int32_t *offsets,
                   int32_t swiglu, void *y, int32_t y_dtype, hipStream_t stream);

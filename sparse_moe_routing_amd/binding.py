@@ -457,7 +457,8 @@ def unpermute_backward(dy, ys, rows, w, shared=None, gate=None, dys=None, stream
 
 
 def quantize_i8(x, stream=None):
-    """(codes [n][K] int8, scales [n] fp32) of the rows of x [n][K] (fp32 or bf16)."""
+    """(codes [n][K] int8, scales [n] fp32) of the rows of x [n][K] (fp32 or bf16), all n of them: of a
+    sorted buffer with more capacity than pairs pass the rows in use, where their number is known."""
     import torch
     dev = x.device
     ctx = _switched(dev, stream)

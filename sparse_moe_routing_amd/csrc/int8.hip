@@ -140,8 +140,8 @@ __device__ __forceinline__ void scaled(const i32x4_t &acc, float sx, const float
 // matrix instructions. Eight waves, two per SIMD: wave w takes the channels of half w % 2 and a
 // quarter of the tile's 16-row subtiles, at most five, so that a tile of n rows costs ceil(n / 64)
 // subtiles of matrix work per wave whatever n is. Waves w and w + 4, on the same SIMD, run one
-// phase apart: while one reads its operands from LDS the other multiplies (65536 rows of 256
-// experts of 2048 x 1024 in a row of calls 194 us in step, 185 so; dense 8192 x 4096 x 4096 131, 126).
+// phase apart: while one reads its operands from LDS the other multiplies (one of many calls in a row:
+// 65536 rows of 256 experts of 2048 x 1024 194 us in step, 185 so; dense 8192 x 4096 x 4096 131, 126).
 //
 // A block's 144 KB of slabs leave one block per CU, so nothing else would cover a unit's start and
 // end: the blocks are persistent, one per CU, and the last slab of a unit is multiplied (and its
@@ -154,18 +154,19 @@ __device__ __forceinline__ void scaled(const i32x4_t &acc, float sx, const float
 // Why these sizes: per slab a CU moves 72 KB into LDS and reads 208 KB of operands for 640 matrix
 // instructions; 320 x 256 is the patch with the least LDS traffic per product whose sums still fit
 // two waves' registers, and at 65536 rows of 256 experts most experts' rows fit one tile, so that
-// their weights cross HBM once. Measured: 65536 rows of 256 experts of 2048 x 1024 with SwiGLU 173 us
-// (1.6 Pop/s; 644 MiB read, the least there is; matrix units busy 39 %, waits 39 %); dense 8192 x 4096
-// x 4096 126 us (2.2 Pop/s). 256-row tiles take 252 us where these take 229 (before
-// the last steps), 128-channel blocks 260, four waves of 128 x 128 318.
+// their weights cross HBM once. Measured, single calls after the caches were filled with other data:
+// 65536 rows of 256 experts of 2048 x 1024 with SwiGLU 173 us (1.6 Pop/s; 644 MiB read, the least
+// there is; matrix units busy 38 %, waits 38 %); dense 8192 x 4096 x 4096 125 us (2.2 Pop/s). Other
+// shapes, each against this one as it was then: 256-row tiles took 10 % longer, 128-channel blocks 14 %,
+// four waves of 128 x 128 39 %.
 //
 // With fewer rows per expert a slab's matrix work is over long before the next slab has landed, and
 // one slab ahead is not enough to keep the weights coming. The deep form (kDeep) takes at most 128
 // rows a tile; the LDS saved holds a third pair of slab buffers, so that two slabs are in flight
 // behind the one in use. A wave counts its loads (always the same number per slab, past the operands
 // they read zero), waits for all but the youngest slab's, and there is one barrier per slab. Measured,
-// 256 experts of 2048 x 1024 with SwiGLU, 31 rows each: 94 us (6.2 TB/s; the wide form 110), skewed
-// 67 (90); dense 512 x 4096 x 4096 27 (39).
+// 256 experts of 2048 x 1024 with SwiGLU, 31 rows each: 94 us (562 MB, 6.0 TB/s; the wide form 110),
+// skewed 67 (90); dense 512 x 4096 x 4096 27 (39).
 constexpr int kBWaves = 8;
 constexpr int kBRows = 320, kBCh = 256;   // rows and weight channels per block
 constexpr int kSlabB = 128;               // bytes (K elements) of a staged row
@@ -549,9 +550,9 @@ __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(
 // kKS waves make a block and split K between them (their integer sums join in LDS, exact in any
 // order) where there is so little to stream that single waves would not cover the chip; each such
 // block takes one unit.
-// Measured: 256 rows over 256 experts of 2048 x 1024 with SwiGLU 53 us (6.3 TB/s of weights; plain
-// instead of non-temporal loads 63, slabs of half cache lines 65 and more); one row of 4096 x 4096 6
-// us.
+// Measured: 256 rows over about 163 of 256 experts of 2048 x 1024 with SwiGLU 53 us (331 MiB read, 6.5
+// TB/s, the rate of reads alone; plain instead of non-temporal loads 63, slabs of half cache lines 65
+// and more); one row of 4096 x 4096 7 us.
 constexpr int kSCh = 32, kRing = 4;
 constexpr int kSlabBytes = kSCh * kSlabB;  // one wave's slab (4 KB)
 constexpr int kStreamBlocks = 10;          // one-wave blocks per CU
@@ -762,7 +763,8 @@ long most_tiles(const I8Params &p, int per) {
 }
 
 // About how many there will be: the experts' counts are on the device, so even routing is taken, and
-// `more` of a tile more per expert once its rows come near a tile's.
+// `more` of a tile more per expert once its rows come near a tile's. n_rows is the caller's capacity, so
+// where an expert shard passes that of all pairs, an expert is taken to have as many rows more.
 double likely_tiles(const I8Params &p, int per, double more) {
     if (!p.offsets) return (p.n_rows + per - 1) / per;
     const double experts = p.E < p.n_rows ? p.E : p.n_rows, each = p.n_rows / experts / per;

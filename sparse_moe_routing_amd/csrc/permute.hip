@@ -8,7 +8,13 @@
 // All of them run token by token over the inverse table `rows`: every element of x, dy, y, dx is
 // touched once, every sorted row once, no atomics, and a token's sums run in rank order whatever
 // the batch. They move bytes and little else, so what bounds them is HBM at large T and the
-// latency of one dependent chain (table entry, row, result) at decode.
+// latency of one dependent chain (table entry, row, result) at decode. A block works on one row whatever
+// its width: rows of a few hundred bytes leave most of its lanes idle (8192 tokens of 64 bf16: the sort
+// 6.4 us, 1.5 TB/s, 65536 rows as integers 21 us; of 256: 8.6 us, 4.4 TB/s, and 26 us).
+//
+// Two measures are quoted: "alone" is a single call after the caches were filled with other data,
+// "in a row" one of many calls over changing operands, where a call's last stores leave the caches
+// under the next one.
 #include "device_common.h"
 #include "kernels.h"
 
@@ -84,8 +90,8 @@ __device__ __forceinline__ void token_rows(const int32_t *rows, int t, int n_row
 
 // Stores of the sorted rows. kStream: past the caches. A prefill chunk's eight copies of its rows are
 // more than the 256 MB behind the L2s hold, and written through the caches they only push each
-// other out (T = 8192 rows of 2048 bf16: 61.8 us, 51.5 streamed; the return's gradient 69.6 and
-// 65.5); a decode round's rows are read back at once and stay in them.
+// other out (in a row, T = 8192 rows of 2048 bf16: 61.8 us, 51.5 streamed; the return's gradient of
+// 4097 tokens 69.6 and 65.5, now 63); a decode round's rows are read back at once and stay in them.
 constexpr size_t kStreamBytes = (size_t)64 << 20;
 template <bool kStream>
 __device__ __forceinline__ void put16(void *p, const uint4 &v) {
@@ -106,7 +112,8 @@ __device__ __forceinline__ void put8(uint16_t *p, const float (&v)[8]) {
 }
 
 // One block per token: its row is read once and stored to its eight places from registers (T = 8192 of
-// 2048 bf16: 288 MiB moved in 60 us, 5.0 TB/s, nearly all of it stores; one launch at T = 4: 5 us).
+// 2048 bf16: 288 MiB moved in 61 us alone, 4.9 TB/s, nearly all of it stores, 52 in a row; one launch
+// at T = 4: 5 us).
 template <class E, bool kStream>
 __global__ __launch_bounds__(kRowThreads) void permute_kernel(const E *x, const int32_t *rows, int H,
                                                               int n_rows, E *xs) {
@@ -124,8 +131,8 @@ __global__ __launch_bounds__(kRowThreads) void permute_kernel(const E *x, const 
 
 // One block per token again: the sum over its eight sorted rows is formed where they arrive, in fp32
 // and in rank order, and rounded once. kWeighted: unpermute (weights, optional shared row);
-// otherwise permute_backward. T = 8192 of 2048 bf16: 322 MiB in 59 us and 289 MiB in 53 us, 5.7 TB/s,
-// between the rates of a large copy (5.1) and of reads alone (6.5).
+// otherwise permute_backward. T = 8192 of 2048 bf16: 322 MiB in 59 us and 289 MiB in 53 us, alone (58
+// and 52 in a row), 5.7 TB/s, between the rates of a large copy (5.1) and of reads alone (6.5).
 template <class E, class O, bool kWeighted>
 __global__ __launch_bounds__(kRowThreads) void unpermute_kernel(const E *ys, const int32_t *rows,
                                                                 const float *w, const E *shared,
@@ -169,7 +176,8 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 // One block per token: dy[t] is read once for its eight scaled copies and its nine dot products with
 // the same rows (fp32 sums: lanes, a butterfly over the wave, then the four waves in order, the
-// same for every batch). T = 4097 of 2048 bf16: 321 MiB in 67 us, 5.0 TB/s, half of it stores.
+// same for every batch). T = 4097 of 2048 bf16: 321 MiB in 67 us alone, 5.0 TB/s, half of it stores
+// (63 in a row).
 template <class E, class O, bool kStream>
 __global__ __launch_bounds__(kRowThreads) void unpermute_bwd_kernel(const O *dy, const E *ys,
                                                                     const int32_t *rows, const float *w,
@@ -271,10 +279,10 @@ __device__ __forceinline__ uint4 codes16(const float (&v)[16], float scale, floa
 
 // One block per row (kSort: per token, its row written to each of its kept sorted rows), 16
 // elements per thread and turn, as many waves as one turn fills (at most four); the row stays in
-// registers between its maximum and its codes, so that it is read once. Measured: 8192 rows of 4096
-// bf16 22.7 us (96 MiB, 4.4 TB/s; a block's loads, its maximum and its stores follow each other, and
-// only the other blocks of the CU fill the gaps), 8192 rows of 2048 sorted to 65536 32 us (163 MiB,
-// 5.3 TB/s).
+// registers between its maximum and its codes, so that it is read once. Measured alone: 8192 rows of
+// 4096 bf16 22.5 us (96 MiB, 4.5 TB/s; a block's loads, its maximum and its stores follow each other,
+// and only the other blocks of the CU fill the gaps), 8192 rows of 2048 sorted to 65536 33 us (163 MiB,
+// 5.2 TB/s).
 template <class E, bool kSort, int kTurns>
 __global__ __launch_bounds__(kRowThreads) void quantize_kernel(const E *x, const int32_t *rows, int K,
                                                                int n_rows, int8_t *q, float *scale) {
