@@ -258,6 +258,63 @@ int moe_matmul_i8(const int8_t *x, const float *x_scale, int32_t n_rows, const i
                   const float *w_scale, int32_t E, int32_t M, int32_t K, const int32_t *offsets,
                   int32_t swiglu, void *y, int32_t y_dtype, hipStream_t stream);
 
+/* Products with 4-bit weights, grouped by expert:
+ *   z[n][m] = sum_g scale[e][g][m] sum_{k in group g} x[n][k] (code[e][m][k] - zero[e][g][m]),
+ *   offsets[e] <= n < offsets[e + 1]
+ * x [n_rows][K] of `dtype`. w [E][M][K/2]: codes 0..15, two per byte along K, the even column in the
+ * low nibble. Groups are `group` (32, 64 or 128) consecutive columns; scale [E][K/group][M] of
+ * `scale_dtype` (MOE_F32 or MOE_BF16), zero [E][K/group][M] one byte each (0..255), or NULL: 8 for
+ * all. A group's scales lie side by side over the channels. All four 16-byte aligned, and y too.
+ * offsets and swiglu as for moe_matmul_i8 (gate rows first; silu(z[n][i]) z[n][I + i]); rows outside
+ * [offsets[0], offsets[E]) are left as they were; offsets are clamped to [0, n_rows], and where they
+ * fall y is unspecified, but nothing outside it is touched.
+ * Products are exact, sums and scales fp32, y is rounded once to `y_dtype`; the order of a sum depends
+ * on the kernel, which is chosen from the sizes (rows of experts taken as spread evenly), so a row's
+ * bits are the same within a kernel and agree between kernels to fp32 rounding. A row that holds an
+ * infinity or a NaN gives NaN or an infinity in its own results only. n_rows: 0..8388608; E: 1..256;
+ * K: 32..16384, a multiple of the group; M: 8..65536, a multiple of 8 (of 16 with swiglu). */
+int moe_matmul_w4(const void *x, int32_t n_rows, int32_t dtype, const uint8_t *w, const void *scale,
+                  int32_t scale_dtype, const uint8_t *zero, int32_t E, int32_t M, int32_t K,
+                  int32_t group, const int32_t *offsets, int32_t swiglu, void *y, int32_t y_dtype,
+                  hipStream_t stream);
+
+/* ---- Training the router -----------------------------------------------------------------------
+ *
+ * Gradients in the logits [T][R] that moe_route ranked: R columns of which the first E are the experts'
+ * (R = E + 1 with the shared expert's gate). T: 0..1048576; E: 8..256; R: E..16384. ids, w and gate are
+ * as moe_route writes them; ids outside [0, E) are dropped. Pointers are 4-byte aligned (bf16 logits
+ * 2-byte, dlogits of moe_route_backward 16-byte, mask at any address). Nothing is kept between calls, sums run in a
+ * fixed order, and everything can be captured in a HIP graph. */
+
+/* The balance loss of a routing, with the experts' counts:
+ *   P[t] = softmax over the E experts of logits[t]; counts[e] = pairs (t, k) with ids[t][k] = e;
+ *   tokens = N = tokens that count;  loss = E sum_e counts[e] / (8 N) (1/N) sum_t P[t][e]
+ * so 1 for an even routing; 0 with N = 0. mask [T] bytes: tokens with 0 do not count (padding), in
+ * any of the sums, whatever their logits and ids hold; NULL: all count. A token whose logits are all
+ * -infinity has P = 0; a NaN or +infinity among the logits of a token that counts makes the loss NaN.
+ * logits of `dtype` (MOE_F32 or MOE_BF16); loss [1] fp32, counts [E] and tokens [1] int32 are
+ * written for T == 0 too. workspace: moe_balance_workspace_bytes(T, E) bytes (0: may be NULL), 4-byte
+ * aligned, of any contents, that the call owns until its kernels finish. */
+size_t moe_balance_workspace_bytes(int32_t T, int32_t E);
+int moe_balance_loss(const void *logits, const int32_t *ids, const uint8_t *mask, int32_t T, int32_t E,
+                     int32_t R, int32_t dtype, float *loss, int32_t *counts, int32_t *tokens,
+                     void *workspace, size_t ws_bytes, hipStream_t stream);
+
+/* Its gradient: dlogits[t][j] = dloss E/N P[t][j] (f[j] - sum_e f[e] P[t][e]) with f = counts / (8 N), of
+ * `dtype`; 0 for tokens that do not count and in columns E..R-1. dloss [1] fp32. counts and tokens
+ * are the forward's, or sums of several ranks' over the same experts (the gradient is then that
+ * of the loss of all their tokens). */
+int moe_balance_loss_backward(const float *dloss, const void *logits, const int32_t *counts,
+                              const int32_t *tokens, const uint8_t *mask, int32_t T, int32_t E,
+                              int32_t R, int32_t dtype, void *dlogits, hipStream_t stream);
+
+/* The gradient of moe_route's weights and gate: dlogits [T][E], with gate and dgate (both or neither)
+ * [T][E + 1], fp32, all of it written:
+ *   dlogits[t][ids[t][k]] = w[t][k] (dw[t][k] - sum_j w[t][j] dw[t][j])  (summed where an id repeats)
+ *   dlogits[t][E] = gate[t] (1 - gate[t]) dgate[t],  0 elsewhere. */
+int moe_route_backward(const float *dw, const float *w, const int32_t *ids, const float *dgate,
+                       const float *gate, int32_t T, int32_t E, float *dlogits, hipStream_t stream);
+
 /* Static description of a status code. */
 const char *moe_status_str(int status);
 

@@ -1,8 +1,8 @@
-"""The row operators in torch's autograd: binding.permute and binding.unpermute go through these
-where a gradient is recorded, so that a training step needs no wiring by hand.
+"""The row operators and the router's in torch's autograd: binding.permute, binding.unpermute,
+binding.balance_loss and MoeLayer.route of given logits go through these where a gradient is recorded,
+so that a training step needs no wiring by hand.
 
-Both gradients are the library's own operators and exact transposes of the forward pass; neither has
-a second derivative (asking for one raises). Imported on first use: binding itself loads torch only
+The gradients are the library's own operators; none has a second derivative (asking for one raises). Imported on first use: binding itself loads torch only
 inside its functions.
 """
 from __future__ import annotations
@@ -47,3 +47,35 @@ class Unpermute(torch.autograd.Function):
         dys, dw, dshared, dgate = binding.unpermute_backward(
             _operand(dy), ys, rows, w, shared, gate, dys=torch.zeros_like(ys))
         return dys, None, dw, dshared, dgate, None
+
+
+class Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, layer, ws, want_logits):
+        z, ids, w, g = layer.route(None, logits.detach(), None, ws, want_logits)
+        ctx.save_for_backward(w, ids, g)
+        ctx.experts = layer.num_experts
+        ctx.mark_non_differentiable(*(t for t in (z, ids) if t is not None))
+        return z, ids, w, g
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dz, dids, dw, dg):
+        w, ids, g = ctx.saved_tensors
+        dgate = None if g is None else dg.contiguous()
+        return binding.route_backward(dw.contiguous(), w, ids, ctx.experts, dgate, g), None, None, None
+
+
+class BalanceLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, ids, num_experts, mask):
+        loss, counts, tokens = binding.balance_loss(logits, ids, num_experts, mask)
+        ctx.save_for_backward(logits, counts, tokens, mask)
+        ctx.mark_non_differentiable(counts, tokens)
+        return loss, counts, tokens
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss, dcounts, dtokens):
+        logits, counts, tokens, mask = ctx.saved_tensors
+        return binding.balance_loss_backward(dloss.contiguous(), logits, counts, tokens, mask), None, None, None

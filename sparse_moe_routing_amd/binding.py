@@ -30,7 +30,9 @@ EXPORTS = ("moe_create", "moe_destroy", "moe_workspace_bytes", "moe_workspace_st
            "moe_route", "moe_bucket", "moe_bucket_rows",
            "moe_forward", "moe_forward_noalloc", "moe_forward_plan", "moe_forward_timed",
            "moe_permute", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
-           "moe_quantize_i8", "moe_permute_i8", "moe_matmul_i8",
+           "moe_quantize_i8", "moe_permute_i8", "moe_matmul_i8", "moe_matmul_w4",
+           "moe_balance_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward",
+           "moe_route_backward",
            "moe_status_str")
 
 
@@ -87,6 +89,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_permute_i8.restype = ctypes.c_int
     lib.moe_matmul_i8.argtypes = [P, P, I32, P, P, I32, I32, I32, P, I32, P, I32, P]
     lib.moe_matmul_i8.restype = ctypes.c_int
+    lib.moe_matmul_w4.argtypes = [P, I32, I32, P, P, I32, P, I32, I32, I32, I32, P, I32, P, I32, P]
+    lib.moe_matmul_w4.restype = ctypes.c_int
+    lib.moe_balance_workspace_bytes.argtypes = [I32, I32]
+    lib.moe_balance_workspace_bytes.restype = SZ
+    lib.moe_balance_loss.argtypes = [P, P, P, I32, I32, I32, I32, P, P, P, P, SZ, P]
+    lib.moe_balance_loss.restype = ctypes.c_int
+    lib.moe_balance_loss_backward.argtypes = [P, P, P, P, P, I32, I32, I32, I32, P, P]
+    lib.moe_balance_loss_backward.restype = ctypes.c_int
+    lib.moe_route_backward.argtypes = [P, P, P, P, P, I32, I32, P, P]
+    lib.moe_route_backward.restype = ctypes.c_int
     lib.moe_forward.argtypes = [P, P, I32, P, P, P, P, P, SZ, P]
     lib.moe_forward.restype = ctypes.c_int
     lib.moe_forward_noalloc.argtypes = [P, P, I32, P, P, P, P, P]
@@ -188,8 +200,19 @@ class MoeLayer:
             return self.workspace(T, device)
 
     def route(self, x=None, logits=None, T=None, ws=None, want_logits=True, stream=None):
-        """(logits [T][R] or None, ids [T][8], w [T][8], g [T] or None) from x or given logits."""
+        """(logits [T][R] or None, ids [T][8], w [T][8], g [T] or None) from x or given logits. w and g
+        are differentiable in given logits [T][R] (not in x); the logits returned are a copy that is
+        not."""
         import torch
+        if logits is not None and x is None and logits.requires_grad and torch.is_grad_enabled():
+            ctx = _switched(logits.device, stream)
+            if ctx is not None:
+                with ctx:
+                    return self.route(None, logits, T, ws, want_logits)
+            from .autograd import Route
+            z = logits if T is None else logits[:T]
+            _want("logits", z, torch.float32, (z.shape[0], self.rows), z.device.index)
+            return Route.apply(z, self, ws, want_logits)
         src = x if x is not None else logits
         T = src.shape[0] if T is None else T
         dev = src.device
@@ -285,8 +308,8 @@ class MoeLayer:
 
 
 # ---------------------------------------------------------------- separate operators
-# Rows sorted by expert and back, their gradients, and products of 8-bit integers, around a
-# caller's own expert products. rows is the [T*8] int32 table of MoeLayer.bucket_rows. Tensors are
+# Rows sorted by expert and back, their gradients, and products with 8-bit or 4-bit weights, around a
+# caller's own expert products or in their place. rows is the [T*8] int32 table of MoeLayer.bucket_rows. Tensors are
 # contiguous and on one device; what is not raises ValueError before anything is enqueued, and a
 # call that the library refuses raises MoeError. Without `stream` the work is enqueued on the
 # current stream of the tensors' device; with it, results are allocated for that stream, and the
@@ -522,6 +545,130 @@ def matmul_i8(x, x_scale, w, w_scale, offsets=None, swiglu=False, dtype=None, y=
                                 _want("y", y, y.dtype, (n, Mo), at), _row_enum("y", y.dtype),
                                 torch._C._cuda_getCurrentRawStream(at)), "moe_matmul_i8")
     return y
+
+
+def matmul_w4(x, w, scale, zero=None, offsets=None, swiglu=False, dtype=None, y=None, stream=None):
+    """y [n][M] = sum_g scale[e][g][m] sum_{k in g} x[n][k] (code[e][m][k] - zero[e][g][m]) for x [n][K]
+    (fp32 or bf16) and 4-bit codes w [E][M][K / 2] uint8 (the even column in the low nibble), e the expert
+    with offsets[e] <= n < offsets[e + 1] (offsets [E + 1] int32 on the device; None: w holds one
+    matrix for all rows). scale [E][K / G][M] fp32 or bf16 for groups of G = 32, 64 or 128 columns; zero
+    [E][K / G][M] uint8, None: 8 for all. swiglu: w holds gate rows, then up rows, and y [n][M / 2] =
+    silu(gate) up. y of `dtype`, bf16 by default; rows of no expert keep what it held. Records no
+    gradient: operands that require one are refused."""
+    import torch
+    dev = x.device
+    ctx = _switched(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return matmul_w4(x, w, scale, zero, offsets, swiglu, dtype, y)
+    if (x.requires_grad or scale.requires_grad) and torch.is_grad_enabled():
+        raise ValueError("matmul_w4 records no gradient: detach x and scale, or use torch.no_grad()")
+    (n, K), (E, M, _), at = x.shape, w.shape, dev.index
+    num, snum, groups = _row_enum("x", x.dtype), _row_enum("scale", scale.dtype), scale.shape[1]
+    if groups == 0 or K % groups:
+        raise ValueError(f"scale: {groups} groups, expected a divisor of {K} columns")
+    px, pw = _want("x", x, x.dtype, (n, K), at), _want("w", w, torch.uint8, (E, M, K // 2), at)
+    ps = _want("scale", scale, scale.dtype, (E, groups, M), at)
+    pz = None if zero is None else _want("zero", zero, torch.uint8, (E, groups, M), at)
+    po = None if offsets is None else _want("offsets", offsets, torch.int32, (E + 1,), at)
+    Mo = M // 2 if swiglu else M
+    if y is None:
+        y = torch.empty((n, Mo), dtype=torch.bfloat16 if dtype is None else dtype, device=dev)
+    elif dtype is not None and y.dtype != dtype:
+        raise ValueError(f"y: dtype {y.dtype}, expected {dtype}")
+    _check(load().moe_matmul_w4(px, n, num, pw, ps, snum, pz, E, M, K, K // groups, po,
+                                1 if swiglu else 0, _want("y", y, y.dtype, (n, Mo), at),
+                                _row_enum("y", y.dtype), torch._C._cuda_getCurrentRawStream(at)),
+           "moe_matmul_w4")
+    return y
+
+
+# ---------------------------------------------------------------- training the router
+# Gradients in the logits that MoeLayer.route ranked; called and checked as the operators above.
+def _want_mask(mask, T, index):
+    import torch
+    if mask is None:
+        return None
+    return _want("mask", mask, torch.uint8 if mask.dtype is torch.uint8 else torch.bool, (T,), index)
+
+
+def balance_loss(logits, ids, num_experts=None, mask=None, stream=None):
+    """(loss, counts [E] int32, tokens int32) of a routing: loss = E sum_e counts[e] / (8 tokens) mean_t P[t][e],
+    P the softmax of the first E = num_experts (by default all) columns of logits [T][R] (fp32 or bf16),
+    counts the pairs of ids [T][8] of each expert. mask [T] (bool or uint8): tokens with 0 do not
+    count. loss and tokens have no dimensions. The loss is differentiable in the logits."""
+    import torch
+    dev = logits.device
+    ctx = _switched(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return balance_loss(logits, ids, num_experts, mask)
+    if logits.requires_grad and torch.is_grad_enabled():
+        from .autograd import BalanceLoss
+        return BalanceLoss.apply(logits, ids, num_experts, mask)
+    (T, R), at = logits.shape, dev.index
+    E = R if num_experts is None else num_experts
+    num = _row_enum("logits", logits.dtype)
+    pz = _want("logits", logits, logits.dtype, (T, R), at)
+    pi, pm = _want("ids", ids, torch.int32, (T, 8), at), _want_mask(mask, T, at)
+    lib = load()
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    counts = torch.empty((max(E, 0),), dtype=torch.int32, device=dev)
+    tokens = torch.empty((), dtype=torch.int32, device=dev)
+    need = lib.moe_balance_workspace_bytes(T, E)
+    ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+    _check(lib.moe_balance_loss(pz, pi, pm, T, E, R, num, loss.data_ptr(), counts.data_ptr(),
+                                tokens.data_ptr(), ws.data_ptr() if need else None, need,
+                                torch._C._cuda_getCurrentRawStream(at)), "moe_balance_loss")
+    return loss, counts, tokens
+
+
+def balance_loss_backward(dloss, logits, counts, tokens, mask=None, dlogits=None, stream=None):
+    """dlogits [T][R], of the logits' type: the gradient of balance_loss. dloss and tokens without
+    dimensions (fp32, int32); counts and tokens may be summed over several ranks' tokens."""
+    import torch
+    dev = logits.device
+    ctx = _switched(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return balance_loss_backward(dloss, logits, counts, tokens, mask, dlogits)
+    (T, R), E, dt, at = logits.shape, counts.numel(), logits.dtype, dev.index
+    num = _row_enum("logits", dt)
+    pd, pz = _want("dloss", dloss, torch.float32, (), at), _want("logits", logits, dt, (T, R), at)
+    pc, pt = _want("counts", counts, torch.int32, (E,), at), _want("tokens", tokens, torch.int32, (), at)
+    pm = _want_mask(mask, T, at)
+    if dlogits is None:
+        dlogits = torch.empty((T, R), dtype=dt, device=dev)
+    _check(load().moe_balance_loss_backward(pd, pz, pc, pt, pm, T, E, R, num,
+                                            _want("dlogits", dlogits, dt, (T, R), at),
+                                            torch._C._cuda_getCurrentRawStream(at)),
+           "moe_balance_loss_backward")
+    return dlogits
+
+
+def route_backward(dw, w, ids, num_experts, dgate=None, gate=None, dlogits=None, stream=None):
+    """dlogits [T][E], with a shared expert's gate [T][E + 1]: the gradient of the weights w [T][8] (and
+    gate [T]) that MoeLayer.route gives for ids [T][8], from dw (and dgate)."""
+    import torch
+    dev = w.device
+    ctx = _switched(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return route_backward(dw, w, ids, num_experts, dgate, gate, dlogits)
+    if (dgate is None) != (gate is None):
+        raise ValueError("dgate and gate: both or neither")
+    T, at, f32 = w.shape[0], dev.index, torch.float32
+    R = num_experts + (0 if gate is None else 1)
+    pd, pw = _want("dw", dw, f32, (T, 8), at), _want("w", w, f32, (T, 8), at)
+    pi = _want("ids", ids, torch.int32, (T, 8), at)
+    pg = None if gate is None else _want("gate", gate, f32, (T,), at)
+    pdg = None if gate is None else _want("dgate", dgate, f32, (T,), at)
+    if dlogits is None:
+        dlogits = torch.empty((T, max(R, 0)), dtype=f32, device=dev)
+    _check(load().moe_route_backward(pd, pw, pi, pdg, pg, T, num_experts,
+                                     _want("dlogits", dlogits, f32, (T, R), at),
+                                     torch._C._cuda_getCurrentRawStream(at)), "moe_route_backward")
+    return dlogits
 
 
 def device_weights(layer: dict, device="cuda") -> dict:

@@ -1,0 +1,298 @@
+// balance.hip - what trains the router: the balance loss of a routing with its gradient, and the
+// gradient of the selection's weights, both in the logits.
+//
+//   P[t] = softmax(z[t][0..E-1]);  c_e = pairs (t, k) with ids[t][k] = e;  N = counted tokens
+//   L = E sum_e (c_e / 8N) (1/N sum_t P[t][e])
+//   dL/dz[t][j] = E / N P[t][j] (f_j - sum_e f_e P[t][e]),  f_e = c_e / 8N
+// The shares of a nearly even routing are nearly 1 / E, and sum_e P = 1: the gradient is formed with
+// the whole numbers c_e E - 8N in place of f_e, so that nothing cancels in it.
+//
+//   w = softmax over the eight chosen logits, g = sigmoid(z[t][E]):
+//   dz[t][ids_k] = w_k (dw_k - sum_j w_j dw_j);  dz[t][E] = g (1 - g) dg;  0 elsewhere
+//
+// All of them read or write the logits' array once and compute a few instructions per element: HBM
+// bounds them for large T, a launch and one dependent chain for small ones.
+#include "device_common.h"
+#include "kernels.h"
+#include "select_core.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kRowLanes = 16;  // lanes that share a token; a wave takes four tokens at a time
+constexpr int kMaxE = 256;
+constexpr int kBalWaves = 16;
+constexpr int kBalTokens = kBalWaves * (kWave / kRowLanes);  // tokens of one pass of a block
+
+// Sum and maximum over the 16 lanes of a token (every lane gets it), by lane moves in a fixed order.
+__device__ __forceinline__ float row_sum(float v) {
+    v += __uint_as_float(partner32<0>(__float_as_uint(v)));
+    v += __uint_as_float(partner32<1>(__float_as_uint(v)));
+    v += __uint_as_float(partner32<2>(__float_as_uint(v)));
+    v += __uint_as_float(partner32<3>(__float_as_uint(v)));
+    return v;
+}
+__device__ __forceinline__ float row_max(float v) {
+    v = fmaxf(v, __uint_as_float(partner32<0>(__float_as_uint(v))));
+    v = fmaxf(v, __uint_as_float(partner32<1>(__float_as_uint(v))));
+    v = fmaxf(v, __uint_as_float(partner32<2>(__float_as_uint(v))));
+    v = fmaxf(v, __uint_as_float(partner32<3>(__float_as_uint(v))));
+    return v;
+}
+
+__device__ __forceinline__ float as_f32(float v) { return v; }
+__device__ __forceinline__ float as_f32(uint16_t v) { return bf16_bits_to_f32(v); }
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(uint16_t *p, float v) { *p = (uint16_t)(pack_bf16(v, 0.0f) & 0xFFFFu); }
+
+// The probabilities of one token in the 16 lanes that share it: lane l holds experts l, l + 16, ...
+// z: the token's logits (not read when !on: then 0 for all). A token whose logits are all -infinity
+// has probabilities 0. A NaN among the logits, or a logit of +infinity, makes them NaN. 2^x of the
+// rounded z log2(e): a probability e^-a carries a relative error of about a 2^-24 on top of the
+// rounding of 2^x itself, less than a hundred steps where it is still a normal number, and next to
+// none where it is large.
+template <class Z, int kI>
+__device__ __forceinline__ void token_probs(const Z *z, bool on, int E, int l, float (&p)[kI]) {
+    constexpr float kL2e = 1.44269502f;
+    const float kNone = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < kI; ++i) {
+        const int e = i * kRowLanes + l;
+        p[i] = on && e < E ? as_f32(z[e]) : kNone;
+    }
+    float m = kNone;
+#pragma unroll
+    for (int i = 0; i < kI; ++i) m = fmaxf(m, p[i]);
+    m = row_max(m);
+    const bool none = m == kNone;
+    const float base = none ? 0.0f : m;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kI; ++i) {
+        p[i] = __builtin_amdgcn_exp2f((p[i] - base) * kL2e);
+        s += p[i];
+    }
+    s = row_sum(s);
+    const float inv = none ? 0.0f : __builtin_amdgcn_rcpf(s);
+#pragma unroll
+    for (int i = 0; i < kI; ++i) p[i] *= inv;
+}
+
+// The loss from the sums of all tokens: thread e < E holds expert e's. For a block of whole waves.
+__device__ __forceinline__ void write_loss(const BalanceParams &p, int e, double probs, int count, int tokens) {
+    __shared__ double part[kBalWaves];
+    const bool mine = e < p.E;
+    const double n = tokens > 0 ? (double)tokens : 1.0;
+    double v = mine ? (double)count * probs : 0.0;
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) v += __shfl_xor(v, d, kWave);
+    if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = v;
+    if (mine) p.counts[e] = count;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double sum = 0.0;
+        for (int i = 0; i < (int)blockDim.x / kWave; ++i) sum += part[i];
+        *p.loss = (float)(sum * p.E / (kTopK * n * n));
+        *p.tokens = tokens;
+    }
+}
+
+// A block's share of the tokens: sums of their probabilities and counts of their pairs. One block: the
+// loss at once; more: the block's row of the partial sums (balance_join_kernel adds them up in order).
+template <class Z, int kI>
+__global__ __launch_bounds__(kBalWaves *kWave) void balance_kernel(BalanceParams p) {
+    __shared__ float sums[kBalWaves][kMaxE];
+    __shared__ int hist[kMaxE];
+    __shared__ int counted;
+    const int lane = lane_id(), wave = threadIdx.x / kWave, l = lane & (kRowLanes - 1);
+    const int t0 = (int)((int64_t)blockIdx.x * p.T / gridDim.x), t1 = (int)((int64_t)(blockIdx.x + 1) * p.T / gridDim.x);
+    if (threadIdx.x < kMaxE) hist[threadIdx.x] = 0;
+    if (threadIdx.x == 0) counted = 0;
+    __syncthreads();
+    for (int i = t0 * kTopK + threadIdx.x; i < t1 * kTopK; i += kBalWaves * kWave) {
+        const int id = p.ids[i];
+        const bool on = !p.mask || p.mask[i / kTopK];
+        if (on && id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
+        if (on && (i & (kTopK - 1)) == 0) atomicAdd(&counted, 1);
+    }
+    const Z *z = reinterpret_cast<const Z *>(p.logits);
+    float acc[kI] = {};
+    for (int t = t0 + wave * (kWave / kRowLanes) + lane / kRowLanes;
+         t - lane / kRowLanes < t1; t += kBalTokens) {  // uniform: a wave's four tokens
+        const bool on = t < t1 && (!p.mask || p.mask[t]);
+        float q[kI];
+        token_probs<Z, kI>(z + (size_t)(t < t1 ? t : t0) * p.R, on, p.E, l, q);
+#pragma unroll
+        for (int i = 0; i < kI; ++i) acc[i] += q[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kI; ++i) {  // the wave's four tokens' lanes
+        acc[i] += __uint_as_float(partner32<4>(__float_as_uint(acc[i])));
+        acc[i] += __uint_as_float(partner32<5>(__float_as_uint(acc[i])));
+        if (lane < kRowLanes) sums[wave][i * kRowLanes + l] = acc[i];
+    }
+    __syncthreads();
+    const int e = threadIdx.x;
+    const bool mine = e < p.E;
+    double s = 0.0;
+    if (mine)
+#pragma unroll
+        for (int w = 0; w < kBalWaves; ++w) s += (double)sums[w][e];
+    if (gridDim.x == 1) {
+        write_loss(p, e, s, mine ? hist[e] : 0, counted);
+        return;
+    }
+    if (mine) {
+        p.part[(size_t)blockIdx.x * p.E + e] = (float)s;
+        p.part_counts[(size_t)blockIdx.x * p.E + e] = hist[e];
+    }
+    if (threadIdx.x == 0) p.part_tokens[blockIdx.x] = counted;
+}
+
+// The blocks' sums, joined in order, and the loss.
+__global__ __launch_bounds__(4 * kMaxE) void balance_join_kernel(BalanceParams p) {
+    __shared__ double sums[3][kMaxE];
+    __shared__ int counts[3][kMaxE];
+    __shared__ int counted;
+    const int e = threadIdx.x & (kMaxE - 1), g = threadIdx.x / kMaxE;
+    if (threadIdx.x == 0) counted = 0;
+    __syncthreads();
+    double s = 0.0;
+    int c = 0;
+    if (e < p.E)
+#pragma unroll 16
+        for (int b = g; b < p.blocks; b += 4) {
+            s += (double)p.part[(size_t)b * p.E + e];
+            c += p.part_counts[(size_t)b * p.E + e];
+        }
+    for (int b = threadIdx.x; b < p.blocks; b += 4 * kMaxE) atomicAdd(&counted, p.part_tokens[b]);
+    if (g > 0) sums[g - 1][e] = s, counts[g - 1][e] = c;
+    __syncthreads();
+    if (g == 0)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) s += sums[i][e], c += counts[i][e];
+    write_loss(p, g == 0 ? e : kMaxE, s, c, counted);
+}
+
+// dlogits, 16 lanes a token; columns past the experts and tokens that do not count get 0.
+template <class Z, int kI>
+__global__ __launch_bounds__(256) void balance_backward_kernel(BalanceBwdParams p) {
+    const int lane = lane_id(), l = lane & (kRowLanes - 1);
+    const int n = *p.tokens;
+    float d[kI];
+#pragma unroll
+    for (int i = 0; i < kI; ++i) {
+        const int e = i * kRowLanes + l;
+        d[i] = e < p.E ? (float)((int64_t)p.counts[e] * p.E - (int64_t)kTopK * n) : 0.0f;
+    }
+    const float factor = n > 0 ? (float)((double)*p.dloss / ((double)kTopK * n * n)) : 0.0f;
+    const Z *z = reinterpret_cast<const Z *>(p.logits);
+    Z *dz = reinterpret_cast<Z *>(p.dlogits);
+    const int per = 256 / kRowLanes;
+    for (int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / kRowLanes; t - lane / kRowLanes < p.T;
+         t += (int64_t)gridDim.x * per) {
+        const bool there = t < p.T, on = there && (!p.mask || p.mask[t]);
+        float q[kI];
+        const size_t at = (size_t)(there ? t : 0) * p.R;
+        token_probs<Z, kI>(z + at, on, p.E, l, q);
+        float mean = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kI; ++i) mean = fmaf(q[i], d[i], mean);
+        mean = row_sum(mean);
+        if (!there) continue;
+#pragma unroll
+        for (int i = 0; i < kI; ++i) {
+            const int e = i * kRowLanes + l;
+            if (e < p.E) put(dz + at + e, on ? factor * (q[i] * (d[i] - mean)) : 0.0f);
+        }
+        for (int c = p.E + l; c < p.R; c += kRowLanes) put(dz + at + c, 0.0f);
+    }
+}
+
+// The gradient of the selection's weights: a block builds the rows of kSelTokens tokens in LDS and
+// stores them as one aligned run. Eight lanes a token, one per rank; an expert that a token names more
+// than once takes the sum of its ranks, in order.
+constexpr int kSelTokens = 32;
+__global__ __launch_bounds__(kSelTokens *kTopK) void select_backward_kernel(SelectBwdParams p) {
+    __shared__ __align__(16) float rows[kSelTokens * (kMaxE + 1)];
+    const int R = p.E + (p.gate ? 1 : 0), tid = threadIdx.x;
+    const int t0 = blockIdx.x * kSelTokens, n = min(kSelTokens, p.T - t0);
+    const int k = tid & (kTopK - 1), j = tid / kTopK;
+    const bool on = j < n;
+    const size_t pair = (size_t)t0 * kTopK + tid;
+    const float w = on ? p.w[pair] : 0.0f, dw = on ? p.dw[pair] : 0.0f;
+    const int id = on ? p.ids[pair] : -1;
+    const float g = on && k == 0 && p.gate ? p.gate[t0 + j] : 0.0f;
+    const float dg = on && k == 0 && p.gate ? p.dgate[t0 + j] : 0.0f;
+    for (int i = tid * 4; i < kSelTokens * R; i += kSelTokens * kTopK * 4)
+        *reinterpret_cast<float4 *>(rows + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float dot = w * dw;
+    dot += __uint_as_float(partner32<0>(__float_as_uint(dot)));
+    dot += __uint_as_float(partner32<1>(__float_as_uint(dot)));
+    dot += __uint_as_float(partner32<2>(__float_as_uint(dot)));
+    const float v = w * (dw - dot);
+    float sum = 0.0f;
+    bool first = true;
+#pragma unroll
+    for (int r = 0; r < kTopK; ++r) {
+        const bool same = __shfl(id, r, kTopK) == id;
+        const float o = __shfl(v, r, kTopK);
+        if (same) sum += o;
+        if (same && r < k) first = false;
+    }
+    __syncthreads();
+    if (on && first && id >= 0 && id < p.E) rows[j * R + id] = sum;
+    if (on && k == 0 && p.gate) rows[j * R + p.E] = g * (1.0f - g) * dg;
+    __syncthreads();
+    float *out = p.dlogits + (size_t)t0 * R;  // t0 R 4 bytes: a multiple of 16
+    const int total = n * R;
+    for (int i = tid * 4; i + 4 <= total; i += kSelTokens * kTopK * 4)
+        *reinterpret_cast<float4 *>(out + i) = *reinterpret_cast<const float4 *>(rows + i);
+    const int rest = total & ~3;
+    if (rest + tid < total) out[rest + tid] = rows[rest + tid];
+}
+
+// logits type and elements per lane
+template <class Go>
+void typed(int dtype, int E, Go go) {
+    auto wide = [&](auto z) {
+        if (E <= 64) go(z, std::integral_constant<int, 4>{});
+        else if (E <= 128) go(z, std::integral_constant<int, 8>{});
+        else go(z, std::integral_constant<int, 16>{});
+    };
+    if (dtype == 0) wide(float{});
+    else wide(uint16_t{});
+}
+
+}  // namespace
+
+int balance_blocks(int T) {
+    const int one = 8 * kBalTokens;  // up to here the block does all in one launch
+    if (T <= one) return 1;
+    const int b = (T + kBalTokens - 1) / kBalTokens;
+    return b < 256 ? b : 256;
+}
+
+hipError_t launch_balance(const BalanceParams &p, int dtype, hipStream_t s) {
+    typed(dtype, p.E, [&](auto z, auto ki) {
+        launch_k(balance_kernel<decltype(z), decltype(ki)::value>, p.blocks, kBalWaves * kWave, 0, s, p);
+    });
+    if (p.blocks > 1) launch_k(balance_join_kernel, 1, 4 * kMaxE, 0, s, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_balance_backward(const BalanceBwdParams &p, int dtype, hipStream_t s) {
+    const int per = 256 / kRowLanes, all = (p.T + per - 1) / per;
+    typed(dtype, p.E, [&](auto z, auto ki) {
+        launch_k(balance_backward_kernel<decltype(z), decltype(ki)::value>, all < 2048 ? all : 2048, 256, 0, s, p);
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_select_backward(const SelectBwdParams &p, hipStream_t s) {
+    launch_k(select_backward_kernel, (p.T + kSelTokens - 1) / kSelTokens, kSelTokens * kTopK, 0, s, p);
+    return hipGetLastError();
+}
+
+}  // namespace moe

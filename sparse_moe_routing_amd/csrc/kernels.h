@@ -170,6 +170,59 @@ struct I8Params {
     int tile_rows;           // most rows of a row tile (set by the launcher)
 };
 
+// Products with 4-bit weights: weight = scale (code - zero), codes two per byte along K.
+struct W4Params {
+    const void *x;           // [n_rows][K]
+    const uint8_t *w;        // [E][M][K / 2]
+    const void *scale;       // [E][K / group][M]
+    const uint8_t *zero;     // [E][K / group][M], or nullptr: 8 everywhere
+    const int32_t *offsets;  // [E + 1], or nullptr: every row is expert 0's
+    void *y;                 // [n_rows][M], with SwiGLU [n_rows][M / 2]
+    int n_rows, E, M, K;
+    int group;               // columns per scale: 32, 64 or 128
+    int scale_f32;           // scale type: 1 fp32, 0 bf16
+    int y_f32;               // type of y
+    int tile_rows;           // most rows of a row tile (set by the launcher)
+};
+
+// The balance loss and its gradient.
+struct BalanceParams {
+    const void *logits;      // [T][R]
+    const int32_t *ids;      // [T][8]
+    const uint8_t *mask;     // [T], or nullptr: every token counts
+    float *loss;             // [1]
+    int32_t *counts;         // [E]
+    int32_t *tokens;         // [1]
+    float *part;             // [blocks][E] partial sums of the probabilities
+    int32_t *part_counts;    // [blocks][E]
+    int32_t *part_tokens;    // [blocks]
+    int T, E, R, blocks;
+};
+struct BalanceBwdParams {
+    const float *dloss;      // [1]
+    const void *logits;      // [T][R]
+    const int32_t *counts;   // [E]
+    const int32_t *tokens;   // [1]
+    const uint8_t *mask;     // [T] or nullptr
+    void *dlogits;           // [T][R]
+    int T, E, R;
+};
+
+// The gradient of the selection's weights.
+struct SelectBwdParams {
+    const float *dw, *w;     // [T][8]
+    const int32_t *ids;      // [T][8]
+    const float *dgate, *gate;  // [T], or both nullptr
+    float *dlogits;          // [T][E], with the gate [T][E + 1]
+    int T, E;
+};
+
+int balance_blocks(int T);  // blocks (rows of partial sums) of a loss over T tokens
+hipError_t launch_balance(const BalanceParams &p, int dtype, hipStream_t s);
+hipError_t launch_balance_backward(const BalanceBwdParams &p, int dtype, hipStream_t s);
+hipError_t launch_select_backward(const SelectBwdParams &p, hipStream_t s);
+hipError_t launch_matmul_w4(const W4Params &p, int x_dtype, bool swiglu, hipStream_t s);
+
 // Element types: 0 fp32, 1 bf16.
 hipError_t launch_permute(const void *x, const int32_t *rows, int T, int H, int n_rows, int dtype,
                           void *xs, hipStream_t s);
