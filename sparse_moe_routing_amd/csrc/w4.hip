@@ -137,10 +137,327 @@ __global__ __launch_bounds__(256) void w4_tile_kernel(W4Params p) {
     }
 }
 
+// ------------------------------------------------------------------------- few rows per expert
+// With a few rows per expert the time is the one read of the weights. A wave takes up to 4 kR rows of one
+// expert and 32 weight channels (with SwiGLU 16 gate and the matching 16 up channels) and streams the
+// channels' codes in slabs of 128 bytes (256 columns), whole cache lines loaded straight into its own
+// ring of slab buffers, with the slab's scales and zero points beside them. The rows come through
+// buffer loads into registers; rows past the tile's read as zero without a memory access.
+// One-wave blocks fill a CU's LDS. They are persistent: a wave walks its units, and the ring takes the
+// next unit's first slabs while the last slabs and the results of the present one are worked on.
+// kKS waves make a block and split K between them (their sums join in LDS, in order) where there is so
+// little to stream that single waves would not cover the chip; each such block takes one unit.
+//
+// Rows sit in the matrix operand so that a lane's first kR sums are those of the tile's rows: token
+// a + 4 b in operand row 4a + b, b < kR. Of every four operand rows only kR hold tokens; in the
+// registers of the others the columns of other steps are kept, and lane moves within the four bring a
+// step's columns into place: with 4 rows a slab takes two loads in place of eight.
+constexpr int kSCh = 32;                   // weight channels of a wave
+constexpr int kSlabB = 128;                // bytes of a channel's codes in a slab
+constexpr int kSlabK = 2 * kSlabB;         // columns
+constexpr int kSteps = kSlabK / kStepK;    // matrix instructions per 16 channels and slab
+constexpr int kCodeBytes = kSCh * kSlabB;  // a slab's codes
+constexpr int kScaleBytes = kWave * 16;    // room for its scales: at most 8 groups of 32 fp32 numbers
+constexpr int kZeroBytes = kWave * 4;      // and zero points
+constexpr uint32_t kPast = 0xFFFFFFF0u;    // a buffer offset past every range
+
+// Position of 16-byte piece pc (0..7) of staged row r: rows 2m and 2m + 1 rotate by m, so that the 16 rows
+// of one operand read lie on distinct banks.
+__device__ __forceinline__ int spos(int r, int pc) { return r * kSlabB + ((pc ^ (r >> 1)) & 7) * 16; }
+
+template <int kCtrl>
+__device__ __forceinline__ uint32_t quad(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xF, 0xF, true);
+}
+template <int kCtrl>
+__device__ __forceinline__ uint4 quad16(const uint4 &v) {
+    return uint4{quad<kCtrl>(v.x), quad<kCtrl>(v.y), quad<kCtrl>(v.z), quad<kCtrl>(v.w)};
+}
+
+// kGen: fp32 scales or zero points; otherwise bf16 scales alone.
+template <class X, bool kSwiglu, int kR, int kKS, bool kGen>
+__global__ __launch_bounds__(kKS *kWave) __attribute__((amdgpu_waves_per_eu(2))) void w4_stream_kernel(W4Params p) {
+    constexpr int kPer = sizeof(X) / 2;  // 16-byte pieces of a row fragment
+    constexpr int kXL = 2 * kR;          // row fragments of a slab
+    // slabs in flight: their rows' registers set the limit
+    constexpr int kRing = kKS > 1 ? 2 : kGen && kXL * kPer >= 8 ? 3 : 4;
+    constexpr int kSlot = kCodeBytes + kScaleBytes + (kGen ? kZeroBytes : 0);
+    // one object per ring slot, so that the compiler can tell loads into one from reads of another
+    __shared__ __align__(16) unsigned char ring0[kKS][kSlot], ring1[kKS][kSlot], ring2[kRing > 2 ? kKS : 1][kRing > 2 ? kSlot : 16],
+        ring3[kRing > 3 ? kKS : 1][kRing > 3 ? kSlot : 16];
+    constexpr int kCols = kSwiglu ? kSCh / 2 : kSCh;  // output channels of a block
+    constexpr int kRows = 4 * kR;
+    constexpr bool kWalk = kKS == 1;
+    const int lane = lane_id(), wave = kKS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+    const int col = lane & 15, q = lane >> 4;
+    auto slot = [&](auto ic) __attribute__((always_inline)) -> unsigned char * {
+        constexpr int B = decltype(ic)::value;
+        return B == 0 ? ring0[wave] : B == 1 ? ring1[wave] : B == 2 ? ring2[wave] : ring3[wave];
+    };
+    const int Mo = kSwiglu ? p.M / 2 : p.M, KB = p.K / 2;
+    const int S = (Mo + kCols - 1) / kCols;
+    TileScan sc;
+    int tiles = (p.n_rows + kRows - 1) / kRows;
+    if (p.offsets) {
+        sc = scan_tiles(p.offsets, p.E, p.n_rows, kRows);
+        tiles = sc.total;
+    }
+    const int units = tiles * S, per = (units + kXcds - 1) / kXcds;
+    const int first = (blockIdx.x % kXcds) * per, last = min(first + per, units), step = gridDim.x / kXcds;
+    int u = first + blockIdx.x / kXcds;
+    if (u >= last) return;  // uniform
+    auto unit = [&](int i) __attribute__((always_inline)) {
+        if (p.offsets) return pick_unit<kRows>(sc, lane, i, S, kCols);
+        const int ti = i / S;
+        return Unit{{0, ti * kRows, min(kRows, p.n_rows - ti * kRows)}, (i - ti * S) * kCols};
+    };
+    // this wave's slabs: s0 .. s0 + share - 1, in whole turns of the ring
+    const int nslab = (p.K + kSlabK - 1) / kSlabK;
+    const int share = (nslab + kKS - 1) / kKS, s0 = wave * share;
+    const int turns = (share + kRing - 1) / kRing * kRing;
+    // segment a of a slab: staged rows 8a .. 8a + 7 (SwiGLU: rows 16 .. 31 are the up channels)
+    uint32_t woff[kSCh / 8];
+    int wk[kSCh / 8];
+#pragma unroll
+    for (int a = 0; a < kSCh / 8; ++a) {
+        const int R = 8 * a + (lane >> 3), c = kSwiglu ? (R & 15) + (R >> 4) * Mo : R;
+        wk[a] = (((lane & 7) ^ (R >> 1)) & 7) * 16;
+        woff[a] = (uint32_t)c * KB + wk[a];
+    }
+    // row fragment j: step j (4 / kR) + xs of the lane's token
+    const int b4 = col & 3, xs = b4 / kR;
+    const uint32_t xoff = ((uint32_t)((col >> 2) + 4 * (b4 % kR)) * p.K + xs * kStepK + 8 * q) * sizeof(X);
+    // scales: groups of a slab, 32 channels each (SwiGLU: 16 gate, 16 up), in 16-byte pieces
+    const int gl = p.group == 128 ? 2 : p.group == 64 ? 1 : 0;  // log2 of the steps of a group
+    const int slabg = kSteps >> gl, groups = p.K / p.group;
+    const bool wide = kGen && p.scale_f32;
+    const int sb = wide ? 4 : 2;                                // bytes of a scale
+    const int sg = lane >> (wide ? 3 : 2), sp = lane & (wide ? 7 : 3), shalf = wide ? 4 : 2;
+    const uint32_t soff = (uint32_t)(sg * p.M + (kSwiglu && sp >= shalf ? Mo : 0)) * sb + (kSwiglu ? sp % shalf : sp) * 16;
+    const int zg = lane >> 3, zp = lane & 7;
+    const uint32_t zoff = (uint32_t)(zg * p.M + (kSwiglu && zp >= 4 ? Mo : 0) + (kSwiglu ? zp % 4 : zp) * 4);
+    // reading them: the word of the lane's channel, and which half of it (fp32: all)
+    const int s_word = col * sb & ~3, s_shift = wide || (col & 1) ? 0 : 16;
+    const uint32_t s_mask = wide ? ~0u : 0xFFFF0000u;
+    const float z_bias = p.zero ? -8.0f : 0.0f;  // without zero points 0s are loaded: 8 - 8
+    uint4 xr[kRing][kXL][kPer];
+    // the wave's slab i of unit v: always the same number of loads (they are counted); pieces at or
+    // past K, slabs past the share and units that do not exist (any = false) read as zero
+    auto issue = [&](auto ic, const Unit &v, int i, bool any) __attribute__((always_inline)) {
+        constexpr int B = decltype(ic)::value;
+        const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(reinterpret_cast<const X *>(p.x) + (size_t)v.t.start * p.K,
+                                                      (uint32_t)v.t.n * (uint32_t)p.K * (uint32_t)sizeof(X));
+        const __amdgpu_buffer_rsrc_t rw =
+            buffer_rsrc(p.w + ((size_t)v.t.e * p.M + v.m0) * KB, (uint32_t)(p.M - v.m0) * (uint32_t)KB);
+        const size_t s_at = (size_t)v.t.e * groups * p.M + v.m0;
+        const uint32_t s_n = (uint32_t)groups * (uint32_t)p.M - (uint32_t)v.m0;
+        const int s = s0 + i;
+        const int left = any && i < share ? KB - s * kSlabB : 0;     // bytes of a channel's codes from this slab on
+        const int gleft = any && i < share ? groups - s * slabg : 0; // groups from this slab on
+#pragma unroll
+        for (int a = 0; a < kSCh / 8; ++a)
+            to_lds16<kBufNT>(rw, slot(ic) + a * 1024, wk[a] < left ? woff[a] + (uint32_t)s * kSlabB : kPast);
+        to_lds16<0>(buffer_rsrc(reinterpret_cast<const unsigned char *>(p.scale) + s_at * sb, s_n * sb), slot(ic) + kCodeBytes,
+                    sg < slabg && sg < gleft ? soff + (uint32_t)(s * slabg) * p.M * sb : kPast);
+        if constexpr (kGen)
+            to_lds4(buffer_rsrc(p.zero + (p.zero ? s_at : 0), p.zero ? s_n : 0u), slot(ic) + kCodeBytes + kScaleBytes,
+                    zg < slabg && zg < gleft ? zoff + (uint32_t)(s * slabg) * p.M : kPast);
+#pragma unroll
+        for (int j = 0; j < kXL; ++j)
+#pragma unroll
+            for (int h = 0; h < kPer; ++h)
+                xr[B][j][h] = __builtin_bit_cast(
+                    uint4, __builtin_amdgcn_raw_buffer_load_b128(
+                               rx,
+                               (int)((j * (4 / kR) + xs) * (kStepK / 2) < left
+                                         ? xoff + (uint32_t)(s * kSlabK + j * (4 / kR) * kStepK) * sizeof(X) + 16 * h
+                                         : kPast),
+                               0, 0));
+    };
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    using I3 = std::integral_constant<int, 3>;
+    // loads of the younger slabs may be outstanding when a slab is used
+    constexpr int kYoung = (kRing - 1) * (kSCh / 8 + 1 + (kGen ? 1 : 0) + kXL * kPer);
+    static_assert(kYoung < 64, "vmcnt has six bits");
+    constexpr int kWait = (kYoung & 15) | 0x0F70 | ((kYoung >> 4) << 14);
+
+    Unit cur = unit(u);
+    issue(I0{}, cur, 0, true);
+    issue(I1{}, cur, 1, true);
+    if constexpr (kRing > 2) issue(I2{}, cur, 2, true);
+    if constexpr (kRing > 3) issue(I3{}, cur, 3, true);
+    for (;;) {
+        u += step;
+        const bool more = kWalk && u < last;
+        const Unit nxt = more ? unit(u) : cur;
+        float acc[2][kR] = {};
+        // one slab, a scale per kG steps
+        auto work = [&](auto ic, auto gc) __attribute__((always_inline)) {
+            constexpr int B = decltype(ic)::value, kG = 1 << decltype(gc)::value;
+            f32x4_t sum[2], rows;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                if (s == kSteps / 2) __builtin_amdgcn_sched_barrier(0);  // registers
+                constexpr int kPack = 4 / kR;  // steps in a row fragment
+                Rows8<X> r;
+                uint4 frag[kPer];
+#pragma unroll
+                for (int h = 0; h < kPer; ++h) {
+                    const uint4 &v = xr[B][s / kPack][h];
+                    frag[h] = kR == 4                   ? v
+                              : kR == 2 && s % 2 == 0   ? quad16<0x44>(v)
+                              : kR == 2                 ? quad16<0xEE>(v)
+                              : s % 4 == 0              ? quad16<0x00>(v)
+                              : s % 4 == 1              ? quad16<0x55>(v)
+                              : s % 4 == 2              ? quad16<0xAA>(v)
+                                                        : quad16<0xFF>(v);
+                }
+                __builtin_memcpy(&r, frag, sizeof(r));
+                uint4 a[Rows8<X>::kParts];
+                r.parts(a);
+                if constexpr (kGen) {
+                    if (s % kG == 0) rows = f32x4_t{};
+#pragma unroll
+                    for (int i = 0; i < Rows8<X>::kParts; ++i)
+                        mma(rows, a[i], uint4{kMinus16th, kMinus16th, kMinus16th, kMinus16th});
+                }
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (s % kG == 0) sum[t] = f32x4_t{};
+                    const uint4 b = codes8(*reinterpret_cast<const uint32_t *>(slot(ic) + t * kTile * kSlabB + spos(col, s) + 4 * q));
+#pragma unroll
+                    for (int i = 0; i < Rows8<X>::kParts; ++i) mma(sum[t], a[i], b);
+                    if (s % kG != kG - 1) continue;
+                    const int at = s / kG * kSCh + t * kTile;
+                    const unsigned char *aux = slot(ic) + kCodeBytes;
+                    float scale, z = 0.0f;
+                    if constexpr (kGen) {
+                        scale = __uint_as_float((*reinterpret_cast<const uint32_t *>(aux + at * sb + s_word) << s_shift) & s_mask);
+                        z = (float)(int)aux[kScaleBytes + at + col] + z_bias;
+                    } else {
+                        scale = bf16_bits_to_f32(*reinterpret_cast<const uint16_t *>(aux + (at + col) * 2));
+                    }
+#pragma unroll
+                    for (int r2 = 0; r2 < kR; ++r2)
+                        acc[t][r2] = fmaf(scale, kGen ? fmaf(z, rows[r2], sum[t][r2]) : sum[t][r2], acc[t][r2]);
+                }
+            }
+        };
+        auto turn = [&](auto ic, int i) __attribute__((always_inline)) {
+            __builtin_amdgcn_s_waitcnt(kWait);
+            __builtin_amdgcn_sched_barrier(0);  // the loads counted above stay on their side of it
+            if (gl == 2) work(ic, I2{});
+            else if (gl == 1) work(ic, I1{});
+            else work(ic, I0{});
+            // The refill goes into the slot that was read: it is requested once the reads have returned
+            // (one past K is answered without a memory access, so latency orders nothing).
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // LDS reads: none outstanding; loads: not waited for
+            __builtin_amdgcn_sched_barrier(0);
+            const bool here = i + kRing < turns;  // uniform
+            issue(ic, here ? cur : nxt, here ? i + kRing : i + kRing - turns, here || more);
+        };
+        int i = 0;
+        do {
+            turn(I0{}, i);
+            turn(I1{}, i + 1);
+            if constexpr (kRing > 2) turn(I2{}, i + 2);
+            if constexpr (kRing > 3) turn(I3{}, i + 3);
+        } while ((i += kRing) < turns);
+        bool mine = true;
+        if constexpr (kKS > 1) {  // join the waves' sums in wave 0, in order
+            __shared__ float red[kKS - 1][2][kR][kWave];
+            mine = wave == 0;
+            if (!mine) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int r = 0; r < kR; ++r) red[wave - 1][t][r][lane] = acc[t][r];
+            }
+            __syncthreads();
+            if (mine) {
+#pragma unroll
+                for (int w = 0; w < kKS - 1; ++w)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int r = 0; r < kR; ++r) acc[t][r] += red[w][t][r][lane];
+            }
+        }
+        if (mine) {
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+                const int n = q + 4 * r;
+                if (n >= cur.t.n) continue;
+#pragma unroll
+                for (int t = 0; t < (kSwiglu ? 1 : 2); ++t) {
+                    const int m = cur.m0 + t * kTile + col;
+                    if (m >= Mo) continue;
+                    float z = 16.0f * acc[t][r];
+                    if constexpr (kSwiglu) z = (z < kFarGate ? silu_far(z) : silu(z)) * (16.0f * acc[1][r]);
+                    const size_t at = (size_t)(cur.t.start + n) * Mo + m;
+                    if (p.y_f32) reinterpret_cast<float *>(p.y)[at] = z;
+                    else reinterpret_cast<uint16_t *>(p.y)[at] = (uint16_t)(pack_bf16(z, 0.0f) & 0xFFFFu);
+                }
+            }
+        }
+        if (!more) break;
+        cur = nxt;
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // no load into this block's LDS outlives it
+}
+
+}  // namespace
+
+namespace {
+
+// The most row tiles of `per` rows that n_rows rows of E experts can make.
+long most_tiles(const W4Params &p, int per) {
+    if (!p.offsets) return (p.n_rows + per - 1) / per;
+    const long parts = p.n_rows / per + (p.E < p.n_rows ? p.E : p.n_rows);
+    return parts < p.n_rows ? parts : p.n_rows;
+}
+
+template <class X, int kR, int kKS>
+void launch_stream(const W4Params &p, bool swiglu, unsigned grid, hipStream_t s) {
+    const bool gen = p.zero || p.scale_f32;
+    if (gen && swiglu) launch_k(w4_stream_kernel<X, true, kR, kKS, true>, grid, kKS * kWave, 0, s, p);
+    else if (gen) launch_k(w4_stream_kernel<X, false, kR, kKS, true>, grid, kKS * kWave, 0, s, p);
+    else if (swiglu) launch_k(w4_stream_kernel<X, true, kR, kKS, false>, grid, kKS * kWave, 0, s, p);
+    else launch_k(w4_stream_kernel<X, false, kR, kKS, false>, grid, kKS * kWave, 0, s, p);
+}
+
+constexpr int kStreamBlocks = 8;  // one-wave blocks per CU (LDS)
+constexpr int kSplit = 8;         // waves that split K where there are few units
+
 }  // namespace
 
 hipError_t launch_matmul_w4(const W4Params &p, int x_dtype, bool swiglu, hipStream_t s) {
-    const int Mo = swiglu ? p.M / 2 : p.M;
+    const int Mo = swiglu ? p.M / 2 : p.M, cus = num_cus();
+    const double experts = p.offsets ? (p.E < p.n_rows ? p.E : p.n_rows) : 1, rows = p.n_rows / experts;
+    if (rows <= 16) {
+        const int r = rows <= 3 ? 1 : rows <= 7 || x_dtype == 0 ? 2 : 4;
+        const int cols = swiglu ? kSCh / 2 : kSCh, S = (Mo + cols - 1) / cols;
+        const long units = most_tiles(p, 4 * r) * S;
+        const bool split = units <= 2 * cus && p.K > kSlabK;
+        const long room = (long)cus * kStreamBlocks;
+        const long blocks = units <= room || split ? units : room;
+        const unsigned grid = (unsigned)((blocks + kXcds - 1) / kXcds * kXcds);
+        auto go = [&](auto x, auto rc) {
+            using X = decltype(x);
+            constexpr int kR = decltype(rc)::value;
+            if (split) launch_stream<X, kR, kSplit>(p, swiglu, grid, s);
+            else launch_stream<X, kR, 1>(p, swiglu, grid, s);
+        };
+        using R1 = std::integral_constant<int, 1>;
+        using R2 = std::integral_constant<int, 2>;
+        using R4 = std::integral_constant<int, 4>;
+        if (x_dtype == 0) r == 1 ? go(float{}, R1{}) : go(float{}, R2{});
+        else r == 1 ? go(uint16_t{}, R1{}) : r == 2 ? go(uint16_t{}, R2{}) : go(uint16_t{}, R4{});
+        return hipGetLastError();
+    }
     const long tiles = p.offsets ? p.n_rows / kTile + (p.E < p.n_rows ? p.E : p.n_rows) : (p.n_rows + kTile - 1) / kTile;
     const long blocks = (tiles * ((Mo + kTile - 1) / kTile) + 3) / 4;
     const unsigned grid = (unsigned)(blocks < 16384 ? blocks : 16384);
