@@ -13,7 +13,7 @@ namespace moe {
 constexpr int kXcds = 8;
 
 // Row tiles of the experts in order: expert e's rows [lo, hi) in as few tiles of at most `per` rows
-// as hold them, of even sizes (multiples of kGrain, by default 16, but for the last). Every wave finds its units by
+// as hold them, of even sizes (multiples of 16 but for the last). Every wave finds its units by
 // itself: lane l sums the tiles of experts 4l .. 4l + 3, a wave scan places them.
 struct RowTile {
     int e, start, n;  // n = 0: there is no such tile
@@ -46,7 +46,6 @@ struct Unit {
 };
 // Unit u of S blocks of `cols` output channels per tile. An expert's units run channel block by
 // channel block, its tiles next to each other: they read the same weights at about the same time.
-template <int kGrain = 16>
 __device__ __forceinline__ Unit pick_unit(const TileScan &s, int lane, int u, int S, int cols) {
     int at = s.at, e = 0, start = 0, n = 0, c = 0;
     bool mine = false;
@@ -57,7 +56,7 @@ __device__ __forceinline__ Unit pick_unit(const TileScan &s, int lane, int u, in
             mine = true;
             e = 4 * lane + i;
             c = (u - at * S) / nt;
-            const int rows = s.hi[i] - s.lo[i], part = ((rows + nt - 1) / nt + kGrain - 1) & ~(kGrain - 1);
+            const int rows = s.hi[i] - s.lo[i], part = ((rows + nt - 1) / nt + 15) & ~15;
             start = s.lo[i] + (u - at * S - c * nt) * part;
             n = min(part, s.hi[i] - start);
         }

@@ -222,6 +222,8 @@ hipError_t launch_balance(const BalanceParams &p, int dtype, hipStream_t s);
 hipError_t launch_balance_backward(const BalanceBwdParams &p, int dtype, hipStream_t s);
 hipError_t launch_select_backward(const SelectBwdParams &p, hipStream_t s);
 hipError_t launch_matmul_w4(const W4Params &p, int x_dtype, bool swiglu, hipStream_t s);
+// its kernel for many rows; tile_rows: a multiple of 64 up to 256
+hipError_t launch_w4_block(const W4Params &p, int x_dtype, bool swiglu, hipStream_t s);
 
 // Element types: 0 fp32, 1 bf16.
 hipError_t launch_permute(const void *x, const int32_t *rows, int T, int H, int n_rows, int dtype,
