@@ -106,24 +106,23 @@ struct W4Block {
             to_lds16<0>(r, sbuf + wave * 1024, in < slabg && g < groups ? (uint32_t)(g * p.M + channel((l & 31) * 8)) * 2 : kPast);
         }
     }
-    // A block barrier that leaves the youngest kYoung loads in flight; the wave's own LDS reads have returned.
-    template <int kYoung>
+    // A block barrier; the wave's loads have landed and its LDS reads have returned.
     __device__ __forceinline__ void top() const {
-        __builtin_amdgcn_s_waitcnt(0x0070 | kYoung);
+        __builtin_amdgcn_s_waitcnt(0x0070);
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("" ::: "memory");
     }
-    __device__ __forceinline__ float scale_at(const unsigned char *sbuf, int g, int R) const {
-        if constexpr (kGen) {
-            const int at = R * sb;
-            const uint32_t v = *reinterpret_cast<const uint32_t *>(sbuf + g * kGroupB + (at & ~3));
-            return __uint_as_float(sb == 4 ? v : (R & 1) ? v & 0xFFFF0000u : v << 16);
-        } else {
-            return bf16_bits_to_f32(*reinterpret_cast<const uint16_t *>(sbuf + g * kGroupB + R * 2));
-        }
+    // A staged scale, as read and as a number.
+    __device__ __forceinline__ uint32_t scale_bits(const unsigned char *sbuf, int g, int R) const {
+        if constexpr (kGen) return *reinterpret_cast<const uint32_t *>(sbuf + g * kGroupB + (R * sb & ~3));
+        else return *reinterpret_cast<const uint16_t *>(sbuf + g * kGroupB + R * 2);
+    }
+    __device__ __forceinline__ float scale_of(uint32_t bits, int R) const {
+        if constexpr (kGen) return __uint_as_float(sb == 4 ? bits : (R & 1) ? bits & 0xFFFF0000u : bits << 16);
+        else return bf16_bits_to_f32(bits);
     }
 
     // The products of slab h of the slab of codes in cb with the slab of rows in xb. kFlush: steps that
@@ -133,6 +132,7 @@ struct W4Block {
                                          const unsigned char *sbuf, const unsigned char *zbuf, int h) const {
         constexpr int kGroups = kXS / kFlush;  // groups of a slab of rows
         constexpr bool kMinus = kGen || F::kMinus24 != 0;
+        constexpr int kVPerM = F::kParts == 3 ? 2 : 4;
         const int l = here(), col = l & 15, q = l >> 4;
         uint4 x[kN][kXS][F::kParts];
         f32x4_t rows[kN][kGroups];
@@ -155,32 +155,81 @@ struct W4Block {
         }
         const int R0 = ch * kBA * kTile + col, step = h * kXS;
         const float z_bias = (p.zero ? 0.0f : 8.0f) - F::kFrom;
+        // A channel subtile's codes are read two subtiles ahead and made operands one ahead; a sum is scaled
+        // just before its registers take the next one, kN matrix instructions after its last: so
+        // the matrix instructions always have something beside them.
+        struct Bits {
+            uint32_t s[kGroups];
+            int z[kGroups];
+        };
+        struct Scales {
+            float s[kGroups], z[kGroups];
+        };
+        auto words = [&](int i, uint32_t (&w)[kXS]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int s = 0; s < kXS; ++s)
+                w[s] = *reinterpret_cast<const uint32_t *>(cb + (ch * kBA + i) * kTile * kSlabB + spos(col, step + s) + 4 * q);
+        };
+        auto bits = [&](int i, Bits &v) __attribute__((always_inline)) {
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                const int at = (step + g * kFlush) >> gl, R = R0 + i * kTile;
+                v.s[g] = scale_bits(sbuf, at, R);
+                v.z[g] = kGen ? (int)zbuf[at * kBCh + R] : 0;
+            }
+        };
+        uint32_t w[2][kXS];
+        Bits raw[2];
+        Scales sc[2];
+        uint4 ops[2][kXS];
+        f32x4_t sum[kN];
+        auto scaled = [&](int i, int g, int j) __attribute__((always_inline)) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float v = sum[j][r];
+                acc[i][j][r] = fmaf(sc[i & 1].s[g], kGen ? fmaf(sc[i & 1].z[g], rows[j][g][r], v) : v, acc[i][j][r]);
+            }
+        };
+        words(0, w[0]);
+        words(1, w[1]);
+        bits(0, raw[0]);
+#pragma unroll
+        for (int s = 0; s < kXS; ++s) ops[0][s] = form.codes(w[0][s]);
 #pragma unroll
         for (int i = 0; i < kBA; ++i) {
-            f32x4_t sum[kN];
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                sc[i & 1].s[g] = scale_of(raw[i & 1].s[g], col);
+                sc[i & 1].z[g] = (float)raw[i & 1].z[g] + z_bias;
+            }
+            if (i + 1 < kBA) bits(i + 1, raw[(i + 1) & 1]);
+            if (i + 2 < kBA) words(i + 2, w[i & 1]);
 #pragma unroll
             for (int s = 0; s < kXS; ++s) {
-                const int R = R0 + i * kTile;
-                const uint4 b = form.codes(*reinterpret_cast<const uint32_t *>(
-                    cb + (ch * kBA + i) * kTile * kSlabB + spos(col, step + s) + 4 * q));
+                if (i + 1 < kBA && s == kXS - 1)
+#pragma unroll
+                    for (int s2 = 0; s2 < kXS; ++s2) ops[(i + 1) & 1][s2] = form.codes(w[(i + 1) & 1][s2]);
 #pragma unroll
                 for (int j = 0; j < kN; ++j) {
-                    if (s % kFlush == 0) sum[j] = kMinus && !kGen ? rows[j][s / kFlush] : f32x4_t{};
+                    if (s % kFlush == 0) {
+                        if (s > 0) scaled(i, s / kFlush - 1, j);
+                        else if (i > 0) scaled(i - 1, kGroups - 1, j);
+                        sum[j] = kMinus && !kGen ? rows[j][s / kFlush] : f32x4_t{};
+                    }
 #pragma unroll
-                    for (int k = 0; k < F::kParts; ++k) mma(sum[j], x[j][s][k], b);
+                    for (int k = 0; k < F::kParts; ++k) mma(sum[j], x[j][s][k], ops[i & 1][s]);
                 }
-                if (s % kFlush != kFlush - 1) continue;
-                const int g = (step + s) >> gl;
-                const float scale = scale_at(sbuf, g, R);
-                float z = 0.0f;
-                if constexpr (kGen) z = (float)(int)zbuf[g * kBCh + R] + z_bias;
-#pragma unroll
-                for (int j = 0; j < kN; ++j)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        acc[i][j][r] = fmaf(scale, kGen ? fmaf(z, rows[j][s / kFlush][r], sum[j][r]) : sum[j][r], acc[i][j][r]);
             }
+            // their order: a few vector instructions before each matrix instruction
+#pragma unroll
+            for (int m = 0; m < kXS * kN * F::kParts; ++m) {
+                __builtin_amdgcn_sched_group_barrier(0x002, kVPerM, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
+#pragma unroll
+        for (int j = 0; j < kN; ++j) scaled(kBA - 1, kGroups - 1, j);
     }
 };
 
@@ -241,8 +290,7 @@ __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(
                 const int nS = end ? 0 : S + 1;
                 auto turn = [&](int h, const unsigned char *xb, unsigned char *nxb, bool close) __attribute__((always_inline)) {
                     const int s = S * B::kSub + h;
-                    if (h == 0 || B::kSub > 4 || !load) b.template top<0>();  // (the codes' load is the youngest, if any)
-                    else b.template top<1>();
+                    b.top();
                     if (h == 0 && load) b.issue_s(nu, nsb, nzb, nS);
                     // the next slab of rows: the unit's, or behind its last turn the next unit's first
                     if (!(close && end)) {
