@@ -182,6 +182,7 @@ struct W4Params {
     int group;               // columns per scale: 32, 64 or 128
     int scale_f32;           // scale type: 1 fp32, 0 bf16
     int y_f32;               // type of y
+    int swiglu;
     int tile_rows;           // most rows of a row tile (set by the launcher)
 };
 
@@ -221,9 +222,11 @@ int balance_blocks(int T);  // blocks (rows of partial sums) of a loss over T to
 hipError_t launch_balance(const BalanceParams &p, int dtype, hipStream_t s);
 hipError_t launch_balance_backward(const BalanceBwdParams &p, int dtype, hipStream_t s);
 hipError_t launch_select_backward(const SelectBwdParams &p, hipStream_t s);
-hipError_t launch_matmul_w4(const W4Params &p, int x_dtype, bool swiglu, hipStream_t s);
+hipError_t launch_matmul_w4(const W4Params &p, int x_dtype, hipStream_t s);
 // its kernel for many rows; tile_rows: a multiple of 64 up to 256
-hipError_t launch_w4_block(const W4Params &p, int x_dtype, bool swiglu, hipStream_t s);
+hipError_t launch_w4_block_bf16(const W4Params &p, hipStream_t s);
+hipError_t launch_w4_block_f32(const W4Params &p, hipStream_t s);
+hipError_t launch_w4_block_round(const W4Params &p, hipStream_t s);  // bf16 rows, weights rounded to bf16
 
 // Element types: 0 fp32, 1 bf16.
 hipError_t launch_permute(const void *x, const int32_t *rows, int T, int H, int n_rows, int dtype,

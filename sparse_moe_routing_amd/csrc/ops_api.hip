@@ -205,8 +205,8 @@ int moe_matmul_w4(const void *x, int32_t n_rows, int32_t dtype, const uint8_t *w
                 {scale, groups * (scale_dtype == MOE_F32 ? 4 : 2)}, {zero, groups},
                 {offsets, (size_t)(E + 1) * 4}}))
         return MOE_ERR_INVALID_ARG;
-    const W4Params p{x, w, scale, zero, offsets, y, n_rows, E, M, K, group, scale_dtype == MOE_F32, y_dtype == MOE_F32, 0};
-    return hip_status(launch_matmul_w4(p, dtype, swiglu != 0, stream));
+    const W4Params p{x, w, scale, zero, offsets, y, n_rows, E, M, K, group, scale_dtype == MOE_F32, y_dtype == MOE_F32, swiglu, 0};
+    return hip_status(launch_matmul_w4(p, dtype, stream));
 }
 
 size_t moe_balance_workspace_bytes(int32_t T, int32_t E) {

@@ -316,7 +316,8 @@ constexpr int kSplit = 8;         // waves that split K where there are few unit
 
 }  // namespace
 
-hipError_t launch_matmul_w4(const W4Params &p, int x_dtype, bool swiglu, hipStream_t s) {
+hipError_t launch_matmul_w4(const W4Params &p, int x_dtype, hipStream_t s) {
+    const bool swiglu = p.swiglu;
     const int Mo = swiglu ? p.M / 2 : p.M, cus = num_cus();
     const double experts = p.offsets ? (p.E < p.n_rows ? p.E : p.n_rows) : 1, rows = p.n_rows / experts;
     if (rows <= 16) {
@@ -342,7 +343,8 @@ hipError_t launch_matmul_w4(const W4Params &p, int x_dtype, bool swiglu, hipStre
     }
     W4Params b = p;
     b.tile_rows = 256;
-    return launch_w4_block(b, x_dtype, swiglu, s);
+    if (x_dtype == 0) return launch_w4_block_f32(b, s);
+    return p.y_f32 ? launch_w4_block_bf16(b, s) : launch_w4_block_round(b, s);
 }
 
 }  // namespace moe
