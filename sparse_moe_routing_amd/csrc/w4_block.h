@@ -85,26 +85,22 @@ struct W4Block {
     __device__ __forceinline__ int channel(int R) const {
         return p.swiglu ? (R >> 7) * 64 + (R & 63) + ((R >> 6) & 1) * Mo : R;
     }
-    // Slab s of a unit's rows: segment g holds rows 8g .. 8g + 7; segments past the tile are not loaded. Even
-    // and odd segments rotate differently; pieces past K read as zero.
-    __device__ __forceinline__ void issue_x(const Unit &u, unsigned char *buf, int s) const {
+    // Slab s of a unit's rows (any: there is one): segment g holds rows 8g .. 8g + 7. Rows past the tile and
+    // pieces past K read as zero without a memory access. Even and odd segments rotate differently.
+    __device__ __forceinline__ void issue_x(const Unit &u, unsigned char *buf, int s, bool any) const {
         const int l = here(), XB = p.K * (int)sizeof(X), pc = ((l & 7) ^ (l >> 4)) * 16;
-        const uint32_t even = (uint32_t)(l >> 3) * XB + pc, odd = even - pc + (pc ^ 64);
 #pragma unroll
         for (int h = 0; h < kPer; ++h) {
-            const int from = (s * kPer + h) * kSlabB, left = XB - from;
-            const __amdgpu_buffer_rsrc_t r =
-                buffer_rsrc(reinterpret_cast<const unsigned char *>(p.x) + (size_t)u.t.start * XB + from, (uint32_t)(u.t.n * XB - from));
-            auto loads = [&](uint32_t e, uint32_t o) __attribute__((always_inline)) {
+            const int from = (s * kPer + h) * kSlabB, left = any ? XB - from : 0;
+            const __amdgpu_buffer_rsrc_t r = buffer_rsrc(reinterpret_cast<const unsigned char *>(p.x) + (size_t)u.t.start * XB + from,
+                                                         left > 0 ? (uint32_t)(u.t.n * XB - from) : 0u);
+            const uint32_t row = (uint32_t)(l >> 3) * XB;
+            const uint32_t even = pc < left ? row + pc : 0x80000000u, odd = (pc ^ 64) < left ? row + (pc ^ 64) : 0x80000000u;
 #pragma unroll
-                for (int a = 0; a < kXSegs; ++a) {
-                    const int g = kXSegs * wave + a;
-                    if (8 * g < u.t.n) to_lds16<0>(r, buf + (h * kRows / 8 + g) * 1024, (g & 1 ? o : e) + (uint32_t)(8 * g) * XB);
-                }
-            };
-            if (left >= kSlabB) loads(even, odd);
-            else if (left > 0) loads(pc < left ? even : 0x80000000u, (pc ^ 64) < left ? odd : 0x80000000u);
-            else loads(0x80000000u, 0x80000000u);
+            for (int a = 0; a < kXSegs; ++a) {
+                const int g = kXSegs * wave + a;
+                to_lds16<0>(r, buf + (h * kRows / 8 + g) * 1024, ((kXSegs & 1 ? g : a) & 1 ? odd : even) + (uint32_t)(8 * g) * XB);
+            }
         }
     }
     // The codes of line S that this wave converts (staged row 32 wave + l / 2, 32 columns of each slab), with
@@ -345,7 +341,7 @@ __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(
     typename B::Codes codes[kSub], ncodes[kSub];
     if constexpr (!kRound) b.issue_s(u, s0, 0);
     b.issue_c(u, codes, 0);
-    b.issue_x(u, x0, 0);
+    b.issue_x(u, x0, 0, true);
     b.convert(codes[0], a0);
     for (;;) {
         i += step;
@@ -365,11 +361,8 @@ __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(
                     const typename B::Codes &c = h < kSub - 1 ? codes[(h + 1) % kSub] : ncodes[0];
                     b.meet();
                     // the next slab of rows: the unit's, or behind its last turn the next unit's first
-                    if (h < kSub - 1 || !end) {
-                        if (s + 1 < b.nslab) b.issue_x(u, nxb, s + 1);
-                    } else if (more) {
-                        b.issue_x(nxt, nxb, 0);
-                    }
+                    const bool over = h == kSub - 1 && end;
+                    b.issue_x(over ? nxt : u, nxb, over ? 0 : s + 1, over ? more : s + 1 < b.nslab);
                     if (!kRound && h == 1) b.issue_s(u, s1, 2 * S + 1);
                     if (h == 2) b.issue_c(end ? nxt : u, ncodes, end ? 0 : S + 1);
                     if (!kRound && h == 3) b.issue_s(end ? nxt : u, s0, end ? 0 : 2 * S + 2);

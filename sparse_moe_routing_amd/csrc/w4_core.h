@@ -27,6 +27,7 @@ struct Form;
 template <>
 struct Form<uint16_t> {
     static constexpr int kParts = 1, kPer = 1;  // operands and 16-byte pieces of a fragment
+    static constexpr int kSplit = 2;            // parts of a slab that the scheduler keeps apart
     static constexpr float kFrom = -16.0f, kUnit = 1.0f;
     static constexpr uint32_t kMinus = 0xBF80BF80u;     // -1
     static constexpr uint32_t kMinus24 = 0xC1C0C1C0u;   // 8 - kFrom of them
@@ -48,7 +49,7 @@ struct Form<uint16_t> {
 // instruction converts to fp32 as that number / 16, exact in its upper half.
 template <>
 struct Form<float> {
-    static constexpr int kParts = 3, kPer = 2;
+    static constexpr int kParts = 3, kPer = 2, kSplit = 4;
     static constexpr float kFrom = 8.0f, kUnit = 1.0f / 16.0f;
     static constexpr uint32_t kMinus = 0xBD80BD80u;  // -1/16
     static constexpr uint32_t kMinus24 = 0;          // 8 - kFrom is 0
