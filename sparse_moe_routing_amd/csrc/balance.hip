@@ -41,26 +41,46 @@ __device__ __forceinline__ float row_max(float v) {
     return v;
 }
 
-__device__ __forceinline__ float as_f32(float v) { return v; }
-__device__ __forceinline__ float as_f32(uint16_t v) { return bf16_bits_to_f32(v); }
-__device__ __forceinline__ void put(float *p, float v) { *p = v; }
-__device__ __forceinline__ void put(uint16_t *p, float v) { *p = (uint16_t)(pack_bf16(v, 0.0f) & 0xFFFFu); }
+// A token's logits as the 16 lanes that share it hold them: kI for each. One by one (kV = 1: lane l holds experts
+// l, l + 16, ...), or where rows begin on 16-byte boundaries in whole 16-byte pieces of kV experts.
+template <class Z, int kI, int kV>
+struct Logits {
+    static constexpr int kPieces = kI / kV;
+    using piece_t = typename std::conditional<kV == 1, Z, uint4>::type;
+    piece_t v[kPieces];
+    __device__ static __forceinline__ int expert(int i, int l) { return i / kV * kV * kRowLanes + l * kV + i % kV; }
+    // nothing is read of a token that is not on, nor past the E experts' pieces
+    __device__ __forceinline__ void load(const Z *z, bool on, int E, int l) {
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            const int e = expert(j * kV, l);
+            v[j] = piece_t{};
+            if (on && e < E) v[j] = *reinterpret_cast<const piece_t *>(z + e);
+        }
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (kV == 1) {
+            if constexpr (sizeof(Z) == 4) return v[i];
+            else return bf16_bits_to_f32(v[i]);
+        } else {
+            const uint4 &p = v[i / kV];
+            const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+            if constexpr (sizeof(Z) == 4) return __uint_as_float(w[i % kV]);
+            else return __uint_as_float(i % 2 ? w[i % kV / 2] & 0xFFFF0000u : w[i % kV / 2] << 16);
+        }
+    }
+};
 
-// The probabilities of one token in the 16 lanes that share it: lane l holds experts l, l + 16, ...
-// z: the token's logits (not read when !on: then 0 for all). A token whose logits are all -infinity
-// has probabilities 0. A NaN among the logits, or a logit of +infinity, makes them NaN. 2^x of the
-// rounded z log2(e): a probability e^-a carries a relative error of about a 2^-24 on top of the
-// rounding of 2^x itself, less than a hundred steps where it is still a normal number, and next to
-// none where it is large.
-template <class Z, int kI>
-__device__ __forceinline__ void token_probs(const Z *z, bool on, int E, int l, float (&p)[kI]) {
+// The probabilities of the token. A token whose logits are all -infinity, or that is not on, has
+// probabilities 0. A NaN among the logits, or a logit of +infinity, makes them NaN. 2^x of the rounded z
+// log2(e): a probability e^-a carries a relative error of about a 2^-24 on top of the rounding of 2^x
+// itself, less than a hundred steps where it is still a normal number, and next to none where it is large.
+template <class Z, int kI, int kV>
+__device__ __forceinline__ void token_probs(const Logits<Z, kI, kV> &z, bool on, int E, int l, float (&p)[kI]) {
     constexpr float kL2e = 1.44269502f;
     const float kNone = -__builtin_inff();
 #pragma unroll
-    for (int i = 0; i < kI; ++i) {
-        const int e = i * kRowLanes + l;
-        p[i] = on && e < E ? as_f32(z[e]) : kNone;
-    }
+    for (int i = 0; i < kI; ++i) p[i] = on && Logits<Z, kI, kV>::expert(i, l) < E ? z.get(i) : kNone;
     float m = kNone;
 #pragma unroll
     for (int i = 0; i < kI; ++i) m = fmaxf(m, p[i]);
@@ -77,6 +97,17 @@ __device__ __forceinline__ void token_probs(const Z *z, bool on, int E, int l, f
     const float inv = none ? 0.0f : __builtin_amdgcn_rcpf(s);
 #pragma unroll
     for (int i = 0; i < kI; ++i) p[i] *= inv;
+}
+
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(uint16_t *p, float v) { *p = (uint16_t)(pack_bf16(v, 0.0f) & 0xFFFFu); }
+template <int kV, class Z>
+__device__ __forceinline__ void put_piece(Z *p, const float *v) {
+    if constexpr (kV == 1) put(p, v[0]);
+    else if constexpr (kV == 4) *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+        *reinterpret_cast<uint4 *>(p) =
+            uint4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
 }
 
 // The loss from the sums of all tokens: thread e < E holds expert e's. For a block of whole waves.
@@ -100,7 +131,7 @@ __device__ __forceinline__ void write_loss(const BalanceParams &p, int e, double
 
 // A block's share of the tokens: sums of their probabilities and counts of their pairs. One block: the
 // loss at once; more: the block's row of the partial sums (balance_join_kernel adds them up in order).
-template <class Z, int kI>
+template <class Z, int kI, int kV>
 __global__ __launch_bounds__(kBalWaves *kWave) void balance_kernel(BalanceParams p) {
     __shared__ float sums[kBalWaves][kMaxE];
     __shared__ int hist[kMaxE];
@@ -118,19 +149,32 @@ __global__ __launch_bounds__(kBalWaves *kWave) void balance_kernel(BalanceParams
     }
     const Z *z = reinterpret_cast<const Z *>(p.logits);
     float acc[kI] = {};
-    for (int t = t0 + wave * (kWave / kRowLanes) + lane / kRowLanes;
-         t - lane / kRowLanes < t1; t += kBalTokens) {  // uniform: a wave's four tokens
-        const bool on = t < t1 && (!p.mask || p.mask[t]);
+    // four tokens a wave, the next four's logits on their way
+    using L = Logits<Z, kI, kV>;
+    const int sub = lane / kRowLanes;
+    auto counts = [&](int t) { return t < t1 && (!p.mask || p.mask[t]); };
+    int t = t0 + wave * (kWave / kRowLanes) + sub;
+    bool on = counts(t);
+    L cur;
+    cur.load(z + (size_t)(t < t1 ? t : t0) * p.R, on, p.E, l);
+    while (t - sub < t1) {  // uniform
+        const int n = t + kBalTokens;
+        const bool non = counts(n);
+        L nxt;
+        nxt.load(z + (size_t)(n < t1 ? n : t0) * p.R, non, p.E, l);
         float q[kI];
-        token_probs<Z, kI>(z + (size_t)(t < t1 ? t : t0) * p.R, on, p.E, l, q);
+        token_probs(cur, on, p.E, l, q);
 #pragma unroll
         for (int i = 0; i < kI; ++i) acc[i] += q[i];
+        t = n;
+        on = non;
+        cur = nxt;
     }
 #pragma unroll
     for (int i = 0; i < kI; ++i) {  // the wave's four tokens' lanes
         acc[i] += __uint_as_float(partner32<4>(__float_as_uint(acc[i])));
         acc[i] += __uint_as_float(partner32<5>(__float_as_uint(acc[i])));
-        if (lane < kRowLanes) sums[wave][i * kRowLanes + l] = acc[i];
+        if (lane < kRowLanes) sums[wave][L::expert(i, l)] = acc[i];
     }
     __syncthreads();
     const int e = threadIdx.x;
@@ -143,47 +187,54 @@ __global__ __launch_bounds__(kBalWaves *kWave) void balance_kernel(BalanceParams
         write_loss(p, e, s, mine ? hist[e] : 0, counted);
         return;
     }
-    if (mine) {
-        p.part[(size_t)blockIdx.x * p.E + e] = (float)s;
-        p.part_counts[(size_t)blockIdx.x * p.E + e] = hist[e];
+    if (e < p.stride) {  // (whole 16-byte pieces: the experts past E have 0)
+        p.part[(size_t)blockIdx.x * p.stride + e] = (float)s;
+        p.part_counts[(size_t)blockIdx.x * p.stride + e] = mine ? hist[e] : 0;
     }
     if (threadIdx.x == 0) p.part_tokens[blockIdx.x] = counted;
 }
 
-// The blocks' sums, joined in order, and the loss.
-__global__ __launch_bounds__(4 * kMaxE) void balance_join_kernel(BalanceParams p) {
-    __shared__ double sums[3][kMaxE];
-    __shared__ int counts[3][kMaxE];
+// The blocks' sums, joined in order, and the loss: 16 rows of partial sums at a time, four experts a thread.
+constexpr int kJoin = 16;
+__global__ __launch_bounds__(kJoin *kMaxE / 4) void balance_join_kernel(BalanceParams p) {
+    __shared__ double sums[kJoin][kMaxE];
+    __shared__ int counts[kJoin][kMaxE];
     __shared__ int counted;
-    const int e = threadIdx.x & (kMaxE - 1), g = threadIdx.x / kMaxE;
+    const int e4 = (threadIdx.x & (kMaxE / 4 - 1)) * 4, g = threadIdx.x / (kMaxE / 4);
     if (threadIdx.x == 0) counted = 0;
     __syncthreads();
-    double s = 0.0;
-    int c = 0;
-    if (e < p.E)
-#pragma unroll 16
-        for (int b = g; b < p.blocks; b += 4) {
-            s += (double)p.part[(size_t)b * p.E + e];
-            c += p.part_counts[(size_t)b * p.E + e];
+    double s[4] = {};
+    int c[4] = {};
+    if (e4 < p.stride)
+#pragma unroll 8
+        for (int b = g; b < p.blocks; b += kJoin) {
+            const float4 v = *reinterpret_cast<const float4 *>(p.part + (size_t)b * p.stride + e4);
+            const int4 n = *reinterpret_cast<const int4 *>(p.part_counts + (size_t)b * p.stride + e4);
+            s[0] += (double)v.x, s[1] += (double)v.y, s[2] += (double)v.z, s[3] += (double)v.w;
+            c[0] += n.x, c[1] += n.y, c[2] += n.z, c[3] += n.w;
         }
-    for (int b = threadIdx.x; b < p.blocks; b += 4 * kMaxE) atomicAdd(&counted, p.part_tokens[b]);
-    if (g > 0) sums[g - 1][e] = s, counts[g - 1][e] = c;
-    __syncthreads();
-    if (g == 0)
+    for (int b = threadIdx.x; b < p.blocks; b += kJoin * kMaxE / 4) atomicAdd(&counted, p.part_tokens[b]);
 #pragma unroll
-        for (int i = 0; i < 3; ++i) s += sums[i][e], c += counts[i][e];
-    write_loss(p, g == 0 ? e : kMaxE, s, c, counted);
+    for (int i = 0; i < 4; ++i) sums[g][e4 + i] = s[i], counts[g][e4 + i] = c[i];
+    __syncthreads();
+    const int e = threadIdx.x;
+    double sum = 0.0;
+    int count = 0;
+    if (e < kMaxE)
+#pragma unroll
+        for (int i = 0; i < kJoin; ++i) sum += sums[i][e], count += counts[i][e];
+    write_loss(p, e, sum, count, counted);
 }
 
 // dlogits, 16 lanes a token; columns past the experts and tokens that do not count get 0.
-template <class Z, int kI>
+template <class Z, int kI, int kV>
 __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceBwdParams p) {
     const int lane = lane_id(), l = lane & (kRowLanes - 1);
     const int n = *p.tokens;
     float d[kI];
 #pragma unroll
     for (int i = 0; i < kI; ++i) {
-        const int e = i * kRowLanes + l;
+        const int e = Logits<Z, kI, kV>::expert(i, l);
         d[i] = e < p.E ? (float)((int64_t)p.counts[e] * p.E - (int64_t)kTopK * n) : 0.0f;
     }
     const float factor = n > 0 ? (float)((double)*p.dloss / ((double)kTopK * n * n)) : 0.0f;
@@ -195,16 +246,24 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceBwdParams 
         const bool there = t < p.T, on = there && (!p.mask || p.mask[t]);
         float q[kI];
         const size_t at = (size_t)(there ? t : 0) * p.R;
-        token_probs<Z, kI>(z + at, on, p.E, l, q);
+        Logits<Z, kI, kV> raw;
+        raw.load(z + at, on, p.E, l);
+        token_probs(raw, on, p.E, l, q);
         float mean = 0.0f;
 #pragma unroll
         for (int i = 0; i < kI; ++i) mean = fmaf(q[i], d[i], mean);
         mean = row_sum(mean);
         if (!there) continue;
 #pragma unroll
-        for (int i = 0; i < kI; ++i) {
-            const int e = i * kRowLanes + l;
-            if (e < p.E) put(dz + at + e, on ? factor * (q[i] * (d[i] - mean)) : 0.0f);
+        for (int i = 0; i < kI; ++i) q[i] = on ? factor * (q[i] * (d[i] - mean)) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kI; i += kV) {
+            const int e = Logits<Z, kI, kV>::expert(i, l);
+            if (e + kV <= p.E) put_piece<kV>(dz + at + e, q + i);
+            else
+#pragma unroll
+                for (int k = 0; k < kV; ++k)
+                    if (e + k < p.E) put(dz + at + e + k, q[i + k]);
         }
         for (int c = p.E + l; c < p.R; c += kRowLanes) put(dz + at + c, 0.0f);
     }
@@ -253,16 +312,22 @@ __global__ __launch_bounds__(kSelTokens *kTopK) void select_backward_kernel(Sele
     if (rest + tid < total) out[rest + tid] = rows[rest + tid];
 }
 
-// logits type and elements per lane
+// logits type, elements per lane and how they are taken: in whole pieces where rows of both arrays begin on their boundaries
 template <class Go>
-void typed(int dtype, int E, Go go) {
-    auto wide = [&](auto z) {
-        if (E <= 64) go(z, std::integral_constant<int, 4>{});
-        else if (E <= 128) go(z, std::integral_constant<int, 8>{});
-        else go(z, std::integral_constant<int, 16>{});
+void typed(int dtype, int E, int R, const void *one, const void *two, Go go) {
+    const int bytes = dtype == 0 ? 4 : 2;
+    const bool whole = (size_t)R * bytes % 16 == 0 && (uintptr_t)one % 16 == 0 && (uintptr_t)two % 16 == 0;
+    auto wide = [&](auto z, auto kv) {
+        if (E <= 64 && decltype(kv)::value <= 4) {
+            if constexpr (decltype(kv)::value <= 4) go(z, std::integral_constant<int, 4>{}, kv);
+        } else if (E <= 128) go(z, std::integral_constant<int, 8>{}, kv);
+        else go(z, std::integral_constant<int, 16>{}, kv);
     };
-    if (dtype == 0) wide(float{});
-    else wide(uint16_t{});
+    using V1 = std::integral_constant<int, 1>;
+    using V4 = std::integral_constant<int, 4>;
+    using V8 = std::integral_constant<int, 8>;
+    if (dtype == 0) whole ? wide(float{}, V4{}) : wide(float{}, V1{});
+    else whole ? wide(uint16_t{}, V8{}) : wide(uint16_t{}, V1{});
 }
 
 }  // namespace
@@ -275,17 +340,17 @@ int balance_blocks(int T) {
 }
 
 hipError_t launch_balance(const BalanceParams &p, int dtype, hipStream_t s) {
-    typed(dtype, p.E, [&](auto z, auto ki) {
-        launch_k(balance_kernel<decltype(z), decltype(ki)::value>, p.blocks, kBalWaves * kWave, 0, s, p);
+    typed(dtype, p.E, p.R, p.logits, nullptr, [&](auto z, auto ki, auto kv) {
+        launch_k(balance_kernel<decltype(z), decltype(ki)::value, decltype(kv)::value>, p.blocks, kBalWaves * kWave, 0, s, p);
     });
-    if (p.blocks > 1) launch_k(balance_join_kernel, 1, 4 * kMaxE, 0, s, p);
+    if (p.blocks > 1) launch_k(balance_join_kernel, 1, kJoin * kMaxE / 4, 0, s, p);
     return hipGetLastError();
 }
 
 hipError_t launch_balance_backward(const BalanceBwdParams &p, int dtype, hipStream_t s) {
     const int per = 256 / kRowLanes, all = (p.T + per - 1) / per;
-    typed(dtype, p.E, [&](auto z, auto ki) {
-        launch_k(balance_backward_kernel<decltype(z), decltype(ki)::value>, all < 2048 ? all : 2048, 256, 0, s, p);
+    typed(dtype, p.E, p.R, p.logits, p.dlogits, [&](auto z, auto ki, auto kv) {
+        launch_k(balance_backward_kernel<decltype(z), decltype(ki)::value, decltype(kv)::value>, all < 2048 ? all : 2048, 256, 0, s, p);
     });
     return hipGetLastError();
 }
