@@ -293,7 +293,7 @@ int moe_matmul_w4(const void *x, int32_t n_rows, int32_t dtype, const uint8_t *w
  * any of the sums, whatever their logits and ids hold; NULL: all count. A token whose logits are all
  * -infinity has P = 0; a NaN or +infinity among the logits of a token that counts makes the loss NaN.
  * logits of `dtype` (MOE_F32 or MOE_BF16); loss [1] fp32, counts [E] and tokens [1] int32 are
- * written for T == 0 too. workspace: moe_balance_workspace_bytes(T, E) bytes (0: may be NULL), 16-byte
+ * written for T == 0 too. workspace: moe_balance_workspace_bytes(T, E) bytes (0: may be NULL), 4-byte
  * aligned, of any contents, that the call owns until its kernels finish. */
 size_t moe_balance_workspace_bytes(int32_t T, int32_t E);
 int moe_balance_loss(const void *logits, const int32_t *ids, const uint8_t *mask, int32_t T, int32_t E,

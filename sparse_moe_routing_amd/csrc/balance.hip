@@ -187,43 +187,37 @@ __global__ __launch_bounds__(kBalWaves *kWave) void balance_kernel(BalanceParams
         write_loss(p, e, s, mine ? hist[e] : 0, counted);
         return;
     }
-    if (e < p.stride) {  // (whole 16-byte pieces: the experts past E have 0)
-        p.part[(size_t)blockIdx.x * p.stride + e] = (float)s;
-        p.part_counts[(size_t)blockIdx.x * p.stride + e] = mine ? hist[e] : 0;
+    if (mine) {
+        p.part[(size_t)blockIdx.x * p.E + e] = (float)s;
+        p.part_counts[(size_t)blockIdx.x * p.E + e] = hist[e];
     }
     if (threadIdx.x == 0) p.part_tokens[blockIdx.x] = counted;
 }
 
-// The blocks' sums, joined in order, and the loss: 16 rows of partial sums at a time, four experts a thread.
-constexpr int kJoin = 16;
-__global__ __launch_bounds__(kJoin *kMaxE / 4) void balance_join_kernel(BalanceParams p) {
-    __shared__ double sums[kJoin][kMaxE];
-    __shared__ int counts[kJoin][kMaxE];
+// The blocks' sums, joined in order, and the loss. (Four experts a thread and 16 rows at a time take longer: 10.1 us
+// against 7.6 for 128 rows, both after the caches were filled with other data.)
+__global__ __launch_bounds__(4 * kMaxE) void balance_join_kernel(BalanceParams p) {
+    __shared__ double sums[3][kMaxE];
+    __shared__ int counts[3][kMaxE];
     __shared__ int counted;
-    const int e4 = (threadIdx.x & (kMaxE / 4 - 1)) * 4, g = threadIdx.x / (kMaxE / 4);
+    const int e = threadIdx.x & (kMaxE - 1), g = threadIdx.x / kMaxE;
     if (threadIdx.x == 0) counted = 0;
     __syncthreads();
-    double s[4] = {};
-    int c[4] = {};
-    if (e4 < p.stride)
-#pragma unroll 8
-        for (int b = g; b < p.blocks; b += kJoin) {
-            const float4 v = *reinterpret_cast<const float4 *>(p.part + (size_t)b * p.stride + e4);
-            const int4 n = *reinterpret_cast<const int4 *>(p.part_counts + (size_t)b * p.stride + e4);
-            s[0] += (double)v.x, s[1] += (double)v.y, s[2] += (double)v.z, s[3] += (double)v.w;
-            c[0] += n.x, c[1] += n.y, c[2] += n.z, c[3] += n.w;
+    double s = 0.0;
+    int c = 0;
+    if (e < p.E)
+#pragma unroll 16
+        for (int b = g; b < p.blocks; b += 4) {
+            s += (double)p.part[(size_t)b * p.E + e];
+            c += p.part_counts[(size_t)b * p.E + e];
         }
-    for (int b = threadIdx.x; b < p.blocks; b += kJoin * kMaxE / 4) atomicAdd(&counted, p.part_tokens[b]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sums[g][e4 + i] = s[i], counts[g][e4 + i] = c[i];
+    for (int b = threadIdx.x; b < p.blocks; b += 4 * kMaxE) atomicAdd(&counted, p.part_tokens[b]);
+    if (g > 0) sums[g - 1][e] = s, counts[g - 1][e] = c;
     __syncthreads();
-    const int e = threadIdx.x;
-    double sum = 0.0;
-    int count = 0;
-    if (e < kMaxE)
+    if (g == 0)
 #pragma unroll
-        for (int i = 0; i < kJoin; ++i) sum += sums[i][e], count += counts[i][e];
-    write_loss(p, e, sum, count, counted);
+        for (int i = 0; i < 3; ++i) s += sums[i][e], c += counts[i][e];
+    write_loss(p, g == 0 ? e : kMaxE, s, c, counted);
 }
 
 // dlogits, 16 lanes a token; columns past the experts and tokens that do not count get 0.
@@ -343,7 +337,7 @@ hipError_t launch_balance(const BalanceParams &p, int dtype, hipStream_t s) {
     typed(dtype, p.E, p.R, p.logits, nullptr, [&](auto z, auto ki, auto kv) {
         launch_k(balance_kernel<decltype(z), decltype(ki)::value, decltype(kv)::value>, p.blocks, kBalWaves * kWave, 0, s, p);
     });
-    if (p.blocks > 1) launch_k(balance_join_kernel, 1, kJoin * kMaxE / 4, 0, s, p);
+    if (p.blocks > 1) launch_k(balance_join_kernel, 1, 4 * kMaxE, 0, s, p);
     return hipGetLastError();
 }
 

@@ -194,11 +194,10 @@ struct BalanceParams {
     float *loss;             // [1]
     int32_t *counts;         // [E]
     int32_t *tokens;         // [1]
-    float *part;             // [blocks][stride] partial sums of the probabilities
-    int32_t *part_counts;    // [blocks][stride]
+    float *part;             // [blocks][E] partial sums of the probabilities
+    int32_t *part_counts;    // [blocks][E]
     int32_t *part_tokens;    // [blocks]
     int T, E, R, blocks;
-    int stride;              // E, up to a multiple of 4
 };
 struct BalanceBwdParams {
     const float *dloss;      // [1]

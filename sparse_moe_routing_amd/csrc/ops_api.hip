@@ -33,8 +33,6 @@ bool rows_ok(const void *p, int32_t n) { return aligned(p, 16) && (p || n == 0);
 // A table or vector that is touched: there and 4-byte aligned.
 bool vec_ok(const void *p, int32_t n = 1) { return aligned(p, 4) && (p || n == 0); }
 
-// A row of the balance loss's partial sums: whole 16-byte pieces.
-int stride_of(int32_t E) { return (E + 3) & ~3; }
 // Logits, which the kernels take element by element: there and aligned to one.
 bool logits_ok(const void *p, int32_t T, int dtype) { return aligned(p, dtype == MOE_F32 ? 4 : 2) && (p || T == 0); }
 
@@ -214,7 +212,7 @@ int moe_matmul_w4(const void *x, int32_t n_rows, int32_t dtype, const uint8_t *w
 size_t moe_balance_workspace_bytes(int32_t T, int32_t E) {
     if (T < 0 || T > kMaxTokens || E < 1 || E > kMaxExperts) return 0;
     const int blocks = balance_blocks(T);
-    return blocks > 1 ? (size_t)blocks * (2 * stride_of(E) + 1) * 4 : 0;
+    return blocks > 1 ? (size_t)blocks * (2 * E + 1) * 4 : 0;
 }
 
 int moe_balance_loss(const void *logits, const int32_t *ids, const uint8_t *mask, int32_t T, int32_t E, int32_t R,
@@ -225,16 +223,16 @@ int moe_balance_loss(const void *logits, const int32_t *ids, const uint8_t *mask
     if (!logits_ok(logits, T, dtype) || !vec_ok(ids, T) || !vec_ok(loss) || !vec_ok(counts) || !vec_ok(tokens))
         return MOE_ERR_INVALID_ARG;
     const size_t need = moe_balance_workspace_bytes(T, E);
-    if (need && (!workspace || !aligned(workspace, 16) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+    if (need && (!workspace || !aligned(workspace, 4) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
     const Span ws(workspace, need);
     if (!apart({{loss, 4}, {counts, (size_t)E * 4}, {tokens, 4}, ws},
                {{logits, row_bytes(T, R, dtype)}, {ids, pair_bytes(T)}, {mask, (size_t)T}}))
         return MOE_ERR_INVALID_ARG;
-    const int blocks = balance_blocks(T), stride = stride_of(E);
+    const int blocks = balance_blocks(T);
     float *part = (float *)workspace;
-    int32_t *part_counts = (int32_t *)(part + (size_t)blocks * stride);
+    int32_t *part_counts = (int32_t *)(part + (size_t)blocks * E);
     const BalanceParams p{logits, ids, mask, loss, counts, tokens, part, part_counts,
-                          part_counts + (size_t)blocks * stride, T, E, R, blocks, stride};
+                          part_counts + (size_t)blocks * E, T, E, R, blocks};
     return hip_status(launch_balance(p, dtype, stream));
 }
 

@@ -331,7 +331,8 @@ double likely_tiles(const W4Params &p, int per, double more) {
 // 28 (split), 15 (split), 10.9 (split), 75, 75, 75; 64 rows: 32, 29, 21 (split), 87, 86, 86; 256 rows: 105, 62, 47, 87,
 // 98, 119; 512 rows: 204, 114, 84, 86, 97, 120; 2048 rows: -, -, -, 169, 98, 120; 4096 rows: -, -, -, 342, 196, 131. 256 experts
 // of 2048 x 1024 with SwiGLU, even routing, 1 row an expert: 39, 45, 52, 108; 6 rows: 87, 72, 73, 150; 16 rows: 186,
-// 134, 123, 151; 32 rows: 343, 228, 192, 169; 64 rows: -, -, -, 248, 197, 197.
+// 134, 123, 151; 32 rows: 343, 228, 192, 169; 64 rows: -, -, -, 248, 197, 197. 256 rows an expert: blocks of 256 rows
+// 408, of 320 (most experts' rows in one) 357.
 struct Choice {
     int r, split, tile_rows;  // 4 r rows of a stream wave, split K or not; or r = 0: rows of a block
 };
@@ -356,7 +357,7 @@ Choice choose(const W4Params &p, int x_dtype, int cus) {
         if (nslab > 1) take(most(ceil(units / cus) * (5.0 + share * (wide ? 1.5 + 1.0 * k : 1.7 + 0.5 * k)), memory) + 2.0, {1 << k, 1, 0});
     }
     const int bcols = p.swiglu ? 128 : 256, SB = (Mo + bcols - 1) / bcols;
-    for (int rows = 64; rows <= (wide ? 128 : 256); rows += 64) {
+    for (int rows = 64; rows <= (wide ? 128 : p.y_f32 ? 256 : 320); rows += 64) {
         const double n = rows / 64, slab = wide ? 0.95 + 0.9 * n : p.y_f32 ? 0.9 + 0.4 * n : 0.85 + 0.27 * n;
         const double unit = (p.K + 63) / 64 * slab + 1.5;
         take(most(ceil(likely_tiles(p, rows, 0.35) * SB / cus) * unit, memory) + 5.0, {0, 0, rows});

@@ -27,15 +27,16 @@ constexpr int kBCh = 256;              // weight channels of a block
 constexpr int kBA = kBCh / 2 / kTile;  // channel subtiles of a wave
 constexpr int kBK = 64;                // columns of a slab
 constexpr int kBS = kBK / kStepK;      // its steps
-constexpr int kSub = kSlabK / kBK;     // slabs in a cache line of a channel's codes
 
 template <class X, bool kGen, bool kRound>
 struct W4Block {
     using F = Form<X>;
     static constexpr int kPer = F::kPer;                        // 128-byte pieces of a row in a slab
     // row subtiles of a wave and rows of a block (registers: exact products with zero points need most)
-    static constexpr int kMaxN = kPer > 1 ? 2 : kGen && !kRound ? 3 : 4, kRows = 4 * kTile * kMaxN;
-    static constexpr int kXSegs = kRows / 8 / kBWaves;          // 1 KB segments of rows per wave and piece
+    static constexpr int kMaxN = kPer > 1 ? 2 : kRound ? 5 : kGen ? 3 : 4, kRows = 4 * kTile * kMaxN;
+    // slabs whose codes a wave loads at once: a cache line's, or half of one
+    static constexpr int kSub = kRound ? 2 : 4, kLineB = kSub * kBK / 2;
+    static constexpr int kXSegs = kRows / 8 / kBWaves;          // 1 KB segments of rows per wave and piece (kMaxN)
     static constexpr int kGroupB = kGen ? 4 * kBCh : 2 * kBCh;  // bytes of a group's scales
     static constexpr int kPairGroups = 4;                       // most groups of two slabs
     static constexpr int kScaleB = kRound ? 16 : kPairGroups * kGroupB;
@@ -58,7 +59,7 @@ struct W4Block {
         slabg = 8 >> gl;
         sb = kGen && p.scale_f32 ? 4 : 2;
         nslab = (p.K + kBK - 1) / kBK;
-        nsuper = (p.K + kSlabK - 1) / kSlabK;
+        nsuper = (p.K + kSub * kBK - 1) / (kSub * kBK);
         kept_read = spos(lane & 15, lane >> 4);
     }
     // The lane number, made anew: what is computed from it stays next to its use instead of in registers
@@ -85,8 +86,10 @@ struct W4Block {
     __device__ __forceinline__ int channel(int R) const {
         return p.swiglu ? (R >> 7) * 64 + (R & 63) + ((R >> 6) & 1) * Mo : R;
     }
-    // Slab s of a unit's rows (any: there is one): segment g holds rows 8g .. 8g + 7. Rows past the tile and
-    // pieces past K read as zero without a memory access. Even and odd segments rotate differently.
+    // Slab s of a unit's rows (any: there is one): segment g holds rows 8g .. 8g + 7; a wave takes kSegs of them,
+    // every eighth. Rows past the tile and pieces past K read as zero without a memory access. Even and odd
+    // segments rotate differently.
+    template <int kSegs>
     __device__ __forceinline__ void issue_x(const Unit &u, unsigned char *buf, int s, bool any) const {
         const int l = here(), XB = p.K * (int)sizeof(X), pc = ((l & 7) ^ (l >> 4)) * 16;
 #pragma unroll
@@ -95,11 +98,12 @@ struct W4Block {
             const __amdgpu_buffer_rsrc_t r = buffer_rsrc(reinterpret_cast<const unsigned char *>(p.x) + (size_t)u.t.start * XB + from,
                                                          left > 0 ? (uint32_t)(u.t.n * XB - from) : 0u);
             const uint32_t row = (uint32_t)(l >> 3) * XB;
-            const uint32_t even = pc < left ? row + pc : 0x80000000u, odd = (pc ^ 64) < left ? row + (pc ^ 64) : 0x80000000u;
+            const int mine = pc ^ (wave & 1 ? 64 : 0);
+            const uint32_t at = mine < left ? row + (uint32_t)mine : 0x80000000u;
 #pragma unroll
-            for (int a = 0; a < kXSegs; ++a) {
-                const int g = kXSegs * wave + a;
-                to_lds16<0>(r, buf + (h * kRows / 8 + g) * 1024, ((kXSegs & 1 ? g : a) & 1 ? odd : even) + (uint32_t)(8 * g) * XB);
+            for (int a = 0; a < kSegs; ++a) {
+                const int g = kBWaves * a + wave;
+                to_lds16<0>(r, buf + (h * kRows / 8 + g) * 1024, at + (uint32_t)(8 * g) * XB);
             }
         }
     }
@@ -110,10 +114,10 @@ struct W4Block {
         uint32_t z, s;
     };
     __device__ __forceinline__ void issue_c(const Unit &u, Codes (&c)[kSub], int S) const {
-        const int l = here(), left = KB - S * kSlabB, m = channel(32 * wave + (l >> 1));
+        const int l = here(), left = KB - S * kLineB, m = channel(32 * wave + (l >> 1));
         const __amdgpu_buffer_rsrc_t r =
             buffer_rsrc(p.w + ((size_t)u.t.e * p.M + u.m0) * KB, (uint32_t)(p.M - u.m0) * (uint32_t)KB);
-        const uint32_t at = (uint32_t)m * KB + (uint32_t)S * kSlabB + (l & 1) * 16;
+        const uint32_t at = (uint32_t)m * KB + (uint32_t)S * kLineB + (l & 1) * 16;
 #pragma unroll
         for (int h = 0; h < kSub; ++h)
             c[h].c = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
@@ -124,7 +128,7 @@ struct W4Block {
                                                           p.zero ? (uint32_t)groups * (uint32_t)p.M - (uint32_t)u.m0 : 0u);
 #pragma unroll
             for (int h = 0; h < kSub; ++h) {
-                const int g = (8 * S + 2 * h + (l & 1)) >> gl;
+                const int g = (2 * (kSub * S + h) + (l & 1)) >> gl;
                 c[h].z = bload1(rz, g < groups ? (uint32_t)(g * p.M + m) : kPast);
             }
         }
@@ -134,7 +138,7 @@ struct W4Block {
                                                           ((uint32_t)groups * (uint32_t)p.M - (uint32_t)u.m0) * sb);
 #pragma unroll
             for (int h = 0; h < kSub; ++h) {
-                const int g = (8 * S + 2 * h + (l & 1)) >> gl, at = (g * p.M + m) * sb;
+                const int g = (2 * (kSub * S + h) + (l & 1)) >> gl, at = (g * p.M + m) * sb;
                 c[h].s = bload4(rs, g < groups ? (uint32_t)(at & ~3) : kPast);
             }
         }
@@ -226,7 +230,7 @@ struct W4Block {
     __device__ __forceinline__ void slab(f32x4_t (&acc)[kBA][kN], const unsigned char *xb, const unsigned char *ab,
                                          const unsigned char *sbuf, int h, const Codes &c, unsigned char *nab) const {
         constexpr int kGroups = kBS / kFlush;  // groups of a slab
-        constexpr int kVPerM = F::kParts == 3 || kRound ? 2 : 3;
+        constexpr int kVPerM = F::kParts == 3 ? 2 : 3;
         const int l = here(), col = l & 15, q = l >> 4, rd = read_at();
         const unsigned char *mine = ab + ch * kBA * kTile * kSlabB;
         f32x4_t sum[kN];
@@ -249,7 +253,7 @@ struct W4Block {
         const Factors k = factors(c);
         uint32_t made[4];
         weights(0);
-        if constexpr (!kRound) bits(0);
+        bits(0);
 #pragma unroll
         for (int s = 0; s < kBS; ++s)
 #pragma unroll
@@ -263,23 +267,19 @@ struct W4Block {
             }
 #pragma unroll
         for (int i = 0; i < kBA; ++i) {
-            if constexpr (!kRound) {
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g) scale[i & 1][g] = scale_of(raw[i & 1][g], col);
-                if (i + 1 < kBA) bits(i + 1);
-            }
+            for (int g = 0; g < kGroups; ++g) scale[i & 1][g] = scale_of(raw[i & 1][g], col);
+            if (i + 1 < kBA) bits(i + 1);
             if (i + 1 < kBA) weights(i + 1);
-            if (kRound || i % 2 == 1) operands(word(c, i / 2), k, i % 2, made);
-            if (!kRound && i % 2 == 1) operands(word(c, i / 2), k, 0, made);
-            if (i % 2 == 1) store(nab, i / 2, made);
+            if (i % 2 == 1) {
+                operands(word(c, i / 2), k, 0, made);
+                operands(word(c, i / 2), k, 1, made);
+                store(nab, i / 2, made);
+            }
 #pragma unroll
             for (int s = 0; s < kBS; ++s)
 #pragma unroll
                 for (int j = 0; j < kN; ++j) {
-                    if constexpr (kRound) {
-                        mma(acc[i][j], x[j][s][0], b[i & 1][s]);
-                        continue;
-                    }
                     if (s % kFlush == 0) {
                         if (s > 0) scaled(i, s / kFlush - 1, j);
                         else if (i > 0) scaled(i - 1, kGroups - 1, j);
@@ -289,7 +289,7 @@ struct W4Block {
                     for (int e = 0; e < F::kParts; ++e) mma(sum[j], x[j][s][e], b[i & 1][s]);
                 }
             // their order: the reads ahead first, then a few vector instructions before each matrix instruction
-            if (i + 1 < kBA) __builtin_amdgcn_sched_group_barrier(0x100, kBS + (kRound ? 0 : kGroups), 0);
+            if (i + 1 < kBA) __builtin_amdgcn_sched_group_barrier(0x100, kBS + kGroups, 0);
 #pragma unroll
             for (int m = 0; m < kBS * kN * F::kParts; ++m) {
                 __builtin_amdgcn_sched_group_barrier(0x002, kVPerM, 0);
@@ -297,9 +297,58 @@ struct W4Block {
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (!kRound)
 #pragma unroll
-            for (int j = 0; j < kN; ++j) scaled(kBA - 1, kGroups - 1, j);
+        for (int j = 0; j < kN; ++j) scaled(kBA - 1, kGroups - 1, j);
+    }
+    // The same with the scales in the operands: the sums stay in the matrix instructions from slab to slab. A step
+    // after the other, so that 320 rows fit.
+    template <int kN>
+    __device__ __forceinline__ void slab_rounded(f32x4_t (&acc)[kBA][kN], const unsigned char *xb, const unsigned char *ab,
+                                                 const Codes &c, unsigned char *nab) const {
+        constexpr int kAll = kBS * kBA;
+        const int rd = read_at();
+        const unsigned char *mine = ab + ch * kBA * kTile * kSlabB, *rows = xb + th * kN * kTile * kSlabB;
+        const Factors k = factors(c);
+        uint4 x[kN], b[3];
+        uint32_t made[4];
+        auto weights = [&](int n) __attribute__((always_inline)) {
+            b[n % 3] = load16(mine + n % kBA * kTile * kSlabB + (rd ^ (64 * (n / kBA))));
+        };
+        auto row = [&](int j, int s) __attribute__((always_inline)) { return load16(rows + j * kTile * kSlabB + (rd ^ (64 * s))); };
+        // the second step's rows: in registers of their own where there are enough, or each as soon as the first
+        // step is done with its register
+        constexpr bool kRoom = kN < 5;
+        uint4 behind[kRoom ? kN : 1];
+        weights(0);
+#pragma unroll
+        for (int j = 0; j < kN; ++j) x[j] = row(j, 0);
+        weights(1);
+#pragma unroll
+        for (int n = 0; n < kAll; ++n) {
+            const int i = n % kBA;
+            if (kRoom && n == kBA)
+#pragma unroll
+                for (int j = 0; j < kN; ++j) x[j] = behind[j % (kRoom ? kN : 1)];
+            if (n + 2 < kAll) weights(n + 2);
+            if (kRoom && n >= kBA - kN && n < kBA) behind[(n - (kBA - kN)) % (kRoom ? kN : 1)] = row(n - (kBA - kN), 1);
+            if (n % 2 == 0) operands(word(c, n / 4), k, n / 2 % 2, made);
+            if (n % 4 == 3) store(nab, n / 4, made);
+#pragma unroll
+            for (int j = 0; j < kN; ++j) {
+                mma(acc[i][j], x[j], b[n % 3]);
+                if (!kRoom && n == kBA - 1) x[j] = row(j, 1);
+            }
+            // their order: the reads ahead first, then a few vector instructions before each matrix instruction
+            if (n + 2 < kAll) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            if (kRoom && n >= kBA - kN && n < kBA) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+#pragma unroll
+            for (int m = 0; m < kN; ++m) {
+                __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                if (!kRoom && n == kBA - 1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
 };
 
@@ -338,10 +387,11 @@ __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(
     int i = first + blockIdx.x / kXcds;
     if (i >= last) return;  // uniform
     Unit u = unit(i);
+    constexpr int kSub = B::kSub;
     typename B::Codes codes[kSub], ncodes[kSub];
     if constexpr (!kRound) b.issue_s(u, s0, 0);
     b.issue_c(u, codes, 0);
-    b.issue_x(u, x0, 0, true);
+    b.template issue_x<B::kXSegs>(u, x0, 0, true);
     b.convert(codes[0], a0);
     for (;;) {
         i += step;
@@ -362,20 +412,24 @@ __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(
                     b.meet();
                     // the next slab of rows: the unit's, or behind its last turn the next unit's first
                     const bool over = h == kSub - 1 && end;
-                    b.issue_x(over ? nxt : u, nxb, over ? 0 : s + 1, over ? more : s + 1 < b.nslab);
+                    if (over) b.template issue_x<B::kXSegs>(nxt, nxb, 0, more);
+                    else b.template issue_x<kN>(u, nxb, s + 1, s + 1 < b.nslab);
                     if (!kRound && h == 1) b.issue_s(u, s1, 2 * S + 1);
-                    if (h == 2) b.issue_c(end ? nxt : u, ncodes, end ? 0 : S + 1);
+                    if (h == kSub - 2) b.issue_c(end ? nxt : u, ncodes, end ? 0 : S + 1);
                     if (!kRound && h == 3) b.issue_s(end ? nxt : u, s0, end ? 0 : 2 * S + 2);
                     if (busy && s < b.nslab) {
-                        b.template slab<kN, kFlush>(acc, xb, ab, sbuf, h, c, nab);
+                        if constexpr (kRound) b.template slab_rounded<kN>(acc, xb, ab, c, nab);
+                        else b.template slab<kN, kFlush>(acc, xb, ab, sbuf, h, c, nab);
                     } else {
                         b.convert(c, nab);
                     }
                 };
                 turn(std::integral_constant<int, 0>{}, x0, x1, a0, a1, s0);
                 turn(std::integral_constant<int, 1>{}, x1, x0, a1, a0, s0);
-                turn(std::integral_constant<int, 2>{}, x0, x1, a0, a1, s1);
-                turn(std::integral_constant<int, 3>{}, x1, x0, a1, a0, s1);
+                if constexpr (kSub > 2) {
+                    turn(std::integral_constant<int, 2>{}, x0, x1, a0, a1, s1);
+                    turn(std::integral_constant<int, 3>{}, x1, x0, a1, a0, s1);
+                }
 #pragma unroll
                 for (int h = 0; h < kSub; ++h) codes[h] = ncodes[h];
             }
@@ -406,7 +460,10 @@ __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(
             else if (B::kMaxN == 2 || sub == 2) run(std::integral_constant<int, 2>{}, fc);
             else if constexpr (B::kMaxN > 2) {
                 if (B::kMaxN == 3 || sub == 3) run(std::integral_constant<int, 3>{}, fc);
-                else if constexpr (B::kMaxN > 3) run(std::integral_constant<int, 4>{}, fc);
+                else if constexpr (B::kMaxN > 3) {
+                    if (B::kMaxN == 4 || sub == 4) run(std::integral_constant<int, 4>{}, fc);
+                    else if constexpr (B::kMaxN > 4) run(std::integral_constant<int, 5>{}, fc);
+                }
             }
         };
         if (kRound || b.gl > 0) sized(std::integral_constant<int, 2>{});
