@@ -175,13 +175,44 @@ def test_grouped_whole_numbers(E, n, M, K, G, xdt, ydt, sdt, zero, hot):
     run_whole(n, E, M, K, G, zero, sdt, xdt, ydt, False, 300 + n, before=n // 9, after=n // 7, hot=hot)
 
 
+# few rows and channels, many columns: K split among the waves of a block, in shares that do not come out even
+@pytest.mark.parametrize("xdt,ydt,sdt,zero", [("bf16", "bf16", "bf16", False), ("bf16", "f32", "f32", True),
+                                              ("f32", "f32", "bf16", False), ("f32", "f32", "bf16", True)])
+@pytest.mark.parametrize("n,M,K,G", [(2, 272, 4224, 128), (4, 64, 16384, 64), (7, 272, 2336, 32), (8, 528, 4096, 128),
+                                     (14, 144, 4224, 64), (16, 256, 8192, 128), (30, 272, 4096, 32),
+                                     (8, 6400, 4224, 64), (15, 6416, 2336, 32)])
+def test_split_columns_whole_numbers(n, M, K, G, xdt, ydt, sdt, zero):
+    run_whole(n, 1, M, K, G, zero, sdt, xdt, ydt, False, 900 + n, dense=True)
+    run_whole(n, 1, M, K, G, zero, sdt, xdt, ydt, True, 950 + n, dense=True)
+
+
+# many rows an expert: blocks of every height, rows that end inside a block's subtiles, with zero points and
+# both scale types on bf16 results (their scales are rounded into the weights, which are exact here)
+MANY = [(1, 2700, 2056, 320, 64), (1, 5000, 1032, 1152, 128), (1, 1300, 4104, 448, 32), (1, 900, 8208, 64, 64),
+        (4, 3300, 2064, 448, 32), (3, 2950, 2056, 256, 128), (40, 9000, 1032, 704, 64), (16, 5100, 1544, 192, 32),
+        (2, 700, 8200, 640, 64), (12, 2000, 4104, 128, 128)]
+
+
+@pytest.mark.parametrize("xdt,ydt,sdt,zero", [("bf16", "bf16", "bf16", False), ("bf16", "bf16", "f32", True),
+                                              ("bf16", "bf16", "bf16", True), ("bf16", "bf16", "f32", False),
+                                              ("bf16", "f32", "bf16", False), ("bf16", "f32", "bf16", True),
+                                              ("f32", "f32", "bf16", False), ("f32", "f32", "f32", True)])
+@pytest.mark.parametrize("E,n,M,K,G", MANY)
+def test_many_rows_whole_numbers(E, n, M, K, G, xdt, ydt, sdt, zero):
+    run_whole(n, E, M, K, G, zero, sdt, xdt, ydt, False, 700 + n, dense=E == 1, before=0 if E == 1 else 3,
+              after=0 if E == 1 else 5)
+    run_whole(n, E, M // 16 * 16, K, G, zero, sdt, xdt, ydt, True, 800 + n, dense=E == 1)
+
+
 @pytest.mark.parametrize("hot", [False, True])
-@pytest.mark.parametrize("E,n,M,K,G", GROUPED[1::2])
+@pytest.mark.parametrize("E,n,M,K,G", GROUPED)
 def test_grouped_swiglu(E, n, M, K, G, hot):
     if M % 16:
         M += 8
     run_whole(n, E, M, K, G, False, "bf16", "bf16", "bf16", True, 400 + n, after=n // 5, hot=hot)
     run_whole(n, E, M, K, G, True, "f32", "f32", "f32", True, 500 + n, hot=hot)
+    run_whole(n, E, M, K, G, False, "bf16", "f32", "bf16", True, 1000 + n, hot=hot)
+    run_whole(n, E, M, K, G, True, "bf16", "bf16", "bf16", True, 1100 + n, hot=hot)
 
 
 @pytest.mark.parametrize("xdt", ["bf16", "f32"])
