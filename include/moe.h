@@ -268,11 +268,15 @@ int moe_matmul_i8(const int8_t *x, const float *x_scale, int32_t n_rows, const i
  * offsets and swiglu as for moe_matmul_i8 (gate rows first; silu(z[n][i]) z[n][I + i]); rows outside
  * [offsets[0], offsets[E]) are left as they were; offsets are clamped to [0, n_rows], and where they
  * fall y is unspecified, but nothing outside it is touched.
- * Products are exact, sums and scales fp32, y is rounded once to `y_dtype`; the order of a sum depends
- * on the kernel, which is chosen from the sizes (rows of experts taken as spread evenly), so a row's
- * bits are the same within a kernel and agree between kernels to fp32 rounding. A row that holds an
- * infinity or a NaN gives NaN or an infinity in its own results only. n_rows: 0..8388608; E: 1..256;
- * K: 32..16384, a multiple of the group; M: 8..65536, a multiple of 8 (of 16 with swiglu). */
+ * Sums are fp32 and y is rounded once to `y_dtype`. With fp32 x or fp32 y the codes, zero points and
+ * rows are multiplied as they are and the scales are applied in fp32. With bf16 x and bf16 y the same
+ * holds for few rows; for many the weights scale (code - zero) are rounded to bf16, each by at most
+ * 2^-8 of itself, so that z moves by at most 2^-8 sum |x w|. Which kernel runs, and with it the order
+ * of the sums, is chosen from the sizes (rows of experts taken as spread evenly): the rest of a
+ * batch, as long as it leaves the sizes alone, does not change a row's bits. 32 sum |x| over a group must stay in
+ * fp32's range. A row that holds an infinity or a NaN gives NaN or an infinity in its own results
+ * only. n_rows: 0..8388608; E: 1..256; K: 32..16384, a multiple of the group; M: 8..65536, a
+ * multiple of 8 (of 16 with swiglu). */
 int moe_matmul_w4(const void *x, int32_t n_rows, int32_t dtype, const uint8_t *w, const void *scale,
                   int32_t scale_dtype, const uint8_t *zero, int32_t E, int32_t M, int32_t K,
                   int32_t group, const int32_t *offsets, int32_t swiglu, void *y, int32_t y_dtype,

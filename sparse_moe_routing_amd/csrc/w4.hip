@@ -1,12 +1,13 @@
 // w4.hip - products with 4-bit weights and a scale (and a zero point) per group of columns, grouped by
 // expert: y[n][m] = sum_g s[g][m] sum_{k in g} x[n][k] (c[m][k] - z[g][m]) for the rows n of expert e.
 //
-// Nothing is rounded on the way to the sums: a code is a whole number, exact in bf16, and a bf16 row
-// element is an operand as it stands; fp32 rows go in as three bf16 parts that add up to all of their 24
-// bits. A group's sum runs in the matrix instructions (16x16x32, fp32 sums), the zero point and the scale
-// are applied to it in fp32: s (sum x (c - b) - (z - b) sum x), b a constant of the operand's form.
+// In the form for few rows nothing is rounded on the way to the sums: a code is a whole number, exact in
+// bf16, and a bf16 row element is an operand as it stands; fp32 rows go in as three bf16 parts that add up to all
+// of their 24 bits. A group's sum runs in the matrix instructions (16x16x32, fp32 sums), the zero point and the
+// scale are applied to it in fp32: s (sum x (c - b) - (z - b) sum x), b a constant of the operand's form.
 // Rows are the A operand and channels the B operand: a lane's accumulators are four rows of one
 // channel, so that one scale serves all of a lane's sums.
+// The form for many rows is in w4_block.h. Which one runs is chosen here, from estimated times.
 #include <math.h>
 
 #include "w4_core.h"
@@ -16,12 +17,18 @@ namespace moe {
 namespace {
 
 // ------------------------------------------------------------------------- few rows per expert
-// With a few rows per expert the time is the one read of the weights. A wave takes up to 4 kR rows of one
+// With a few rows per expert the time is the one read of the weights: HBM bounds it. Measured (us, one
+// call over changing operands): 256 experts of 2048 x 1024 with 32 tokens' 256 rows 36 (178 MB, 5.0 TB/s), one
+// row of 4096 x 65536 with zero points 45 (147 MB, 3.3 TB/s: the loads wait beside the operands' instructions,
+// which are those of four rows), 4 rows of 2048 x 1024 8.4 and 32 rows of 4096 x 4096 10.1 (a launch and one chain
+// of loads).
+//
+// A wave takes up to 4 kR rows of one
 // expert and 32 weight channels (with SwiGLU 16 gate and the matching 16 up channels) and streams the
 // channels' codes in slabs of 128 bytes (256 columns), whole cache lines loaded straight into its own
 // ring of slab buffers, with the slab's scales and zero points beside them. The rows come through
 // buffer loads into registers; rows past the tile's read as zero without a memory access.
-// One-wave blocks fill a CU's LDS. They are persistent: a wave walks its units, and the ring takes the
+// One-wave blocks fill a CU's LDS, eight of them. They are persistent: a wave walks its units, and the ring takes the
 // next unit's first slabs while the last slabs and the results of the present one are worked on.
 // kKS waves make a block and split K between them (their sums join in LDS, in order) where there is so
 // little to stream that single waves would not cover the chip; each such block takes one unit.
@@ -31,6 +38,9 @@ namespace {
 // 4a + kR b + r holds token a + 4 r, b steps on. All four are multiplied with a step's codes, and
 // of the four sums of a lane those are taken whose columns are the step's: a sum is only continued by
 // a step of the same place. The rows' own sums, for the zero points, need one instruction for 4 / kR steps.
+// (Against one 16 x 16 tile a wave with the rows loaded as they lie: one row 183 -> 45 us, 32 tokens over 256
+// experts 148 -> 36. Moving the sums between lanes in place of choosing among them takes 49 for the latter, two
+// tiles of 16 rows a wave spill.)
 constexpr int kSCh = 32;                   // weight channels of a wave
 constexpr int kSteps = kSlabK / kStepK;    // matrix instructions per 16 channels and slab
 constexpr int kCodeBytes = kSCh * kSlabB;  // a slab's codes

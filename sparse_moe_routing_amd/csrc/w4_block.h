@@ -1,14 +1,29 @@
 // w4_block.h - products with 4-bit weights for many rows (w4.hip has the arithmetic and the forms for
 // few).
 //
-// A block multiplies up to 256 rows (fp32: 128) of one expert by 256 weight channels (with SwiGLU 128 gate
+// A block multiplies the rows of one expert, up to 320 of them, by 256 weight channels (with SwiGLU 128 gate
 // channels and the 128 up channels that go with them), 64 columns at a time: a slab. Rows are loaded
-// straight into LDS, whole cache lines, double-buffered. Codes come to registers, whole cache lines of
-// four slabs at once, and each wave turns an eighth of a slab's into operands, which it puts into LDS for
-// all of them while the slab before is multiplied: every code is converted once per block, as exactly
-// code - zero (that / 16 without zero points), so that the products need nothing but the scale.
+// straight into LDS, whole cache lines, double-buffered. Codes come to registers, whole cache lines (or
+// halves) of several slabs at once, and each wave turns an eighth of a slab's into operands, which it puts into LDS for
+// all of them while the slab before is multiplied: every code is converted once per block.
 // Eight waves, two per SIMD: wave w takes the channels of half w % 2 and a quarter of the tile's 16-row
 // subtiles, at most kMaxN.
+//
+// Instructions bound it: a SIMD takes two vector instructions beside each matrix instruction of 16 cycles
+// for nothing, and every further one costs nearly its own time. Hence two forms.
+//   Exact (fp32 rows or results): an operand is the whole number code - zero (that / 16 without zero
+//   points), and each group's sums are scaled in fp32: with groups of 64 or more two vector instructions for
+//   each matrix instruction (four rows of a channel, two steps), the conversion on top. Up to 256 rows, 192 with
+//   zero points or fp32 scales, 128 of fp32 rows: what the registers hold.
+//   kRound (bf16 rows and results): an operand is scale (code - zero) rounded to bf16, as a layer of bf16
+//   weights would hold it, and the sums stay in the matrix instructions over all of K: the conversion is all that
+//   stands beside them, and 320 rows fit. The rounding moves a result by at most 2^-8 sum |x w|; with normal
+//   data by 0.0011 of its norm, where rounding the result itself takes 0.0017.
+// Measured (us): 8192 x 4096 x 4096 exact with the codes turned over by each multiplying wave 318, with one
+// conversion a block 281, rounded 263 (1045 TFLOP/s; a large bf16 library product of that shape reaches 1310).
+// 65536 rows over 256 experts of 2048 x 1024 rounded, 256 rows a block 408, 320 (all of most experts' rows) 341
+// to 357. Of the 281, by leaving work out: 234 without the loads of the rows, 261 without those of
+// the codes, 247 without the conversion, 189 without all three.
 //
 // The blocks are persistent, one per CU: the last slab of a unit is multiplied, and its results are stored,
 // while the first slabs of the block's next unit load.
@@ -36,7 +51,7 @@ struct W4Block {
     static constexpr int kMaxN = kPer > 1 ? 2 : kRound ? 5 : kGen ? 3 : 4, kRows = 4 * kTile * kMaxN;
     // slabs whose codes a wave loads at once: a cache line's, or half of one
     static constexpr int kSub = kRound ? 2 : 4, kLineB = kSub * kBK / 2;
-    static constexpr int kXSegs = kRows / 8 / kBWaves;          // 1 KB segments of rows per wave and piece (kMaxN)
+    static constexpr int kXSegs = kRows / 8 / kBWaves;          // 1 KB segments of rows per wave and piece
     static constexpr int kGroupB = kGen ? 4 * kBCh : 2 * kBCh;  // bytes of a group's scales
     static constexpr int kPairGroups = 4;                       // most groups of two slabs
     static constexpr int kScaleB = kRound ? 16 : kPairGroups * kGroupB;
@@ -223,9 +238,9 @@ struct W4Block {
     }
 
     // The products of slab h of a line: rows in xb, operands in ab. kFlush: steps that share a scale (at most
-    // those of a slab). Beside them the codes c of the slab behind become operands in nab. An operand is read one subtile ahead; a sum is scaled just before
-    // its registers take the next one, kN matrix instructions after its last: so the matrix
-    // instructions always have something beside them.
+    // those of a slab). Beside them the codes c of the slab behind become operands in nab. An operand is read one
+    // subtile ahead; a sum is scaled just before its registers take the next one, kN matrix
+    // instructions after its last: so the matrix instructions always have something beside them.
     template <int kN, int kFlush>
     __device__ __forceinline__ void slab(f32x4_t (&acc)[kBA][kN], const unsigned char *xb, const unsigned char *ab,
                                          const unsigned char *sbuf, int h, const Codes &c, unsigned char *nab) const {
@@ -401,7 +416,7 @@ __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(
             constexpr int kN = decltype(nc)::value, kFlush = decltype(fc)::value;
             const bool busy = b.th * kN * kTile < u.t.n;  // uniform: the wave has rows
             f32x4_t acc[kBA][kN] = {};
-            // Line S of the codes: four slabs. Past K nothing is multiplied, but the buffers take their turns.
+            // Line S of the codes: kSub slabs. Past K nothing is multiplied, but the buffers take their turns.
             for (int S = 0; S < b.nsuper; ++S) {
                 const bool end = S + 1 >= b.nsuper;
                 auto turn = [&](auto hc, const unsigned char *xb, unsigned char *nxb, const unsigned char *ab, unsigned char *nab,
