@@ -143,40 +143,49 @@ __global__ __launch_bounds__(kBalWaves *kWave) void balance_kernel(BalanceParams
     __shared__ float sums[kBalWaves][kMaxE];
     __shared__ int hist[kMaxE];
     __shared__ int counted;
-    const int lane = lane_id(), wave = threadIdx.x / kWave, l = lane & (kRowLanes - 1);
-    const int t0 = (int)((int64_t)blockIdx.x * p.T / gridDim.x), t1 = (int)((int64_t)(blockIdx.x + 1) * p.T / gridDim.x);
+    const int lane = lane_id(), wave = threadIdx.x / kWave, l = lane & (kRowLanes - 1), sub = lane / kRowLanes;
     if (threadIdx.x < kMaxE) hist[threadIdx.x] = 0;
     if (threadIdx.x == 0) counted = 0;
-    __syncthreads();
-    for (int i = t0 * kTopK + threadIdx.x; i < t1 * kTopK; i += kBalWaves * kWave) {
-        const int id = p.ids[i];
-        const bool on = !p.mask || p.mask[i / kTopK];
-        if (on && id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
-        if (on && (i & (kTopK - 1)) == 0) atomicAdd(&counted, 1);
-    }
     const Z *z = reinterpret_cast<const Z *>(p.logits);
     float acc[kI] = {};
-    // four tokens a wave, the next four's logits on their way
+    int n = 0;
+    // four tokens a wave, the next four's logits and ids on their way (lanes 0 .. 31: a pair each)
     using L = Logits<Z, kI, kV>;
-    const int sub = lane / kRowLanes;
-    auto counts = [&](int t) { return t < t1 && (!p.mask || p.mask[t]); };
-    int t = t0 + wave * (kWave / kRowLanes) + sub;
+    const int step = (int)gridDim.x * kBalTokens;
+    auto counts = [&](int t) { return t < p.T && (!p.mask || p.mask[t]); };
+    auto pair = [&](int t, uint64_t who) {
+        const int k = t - sub + lane / kTopK;  // the pair's token
+        return lane < 4 * kTopK && (who >> (lane / kTopK * kRowLanes) & 1) ? p.ids[(size_t)k * kTopK + (lane & (kTopK - 1))] : -1;
+    };
+    int t = blockIdx.x * kBalTokens + wave * (kWave / kRowLanes) + sub;
     bool on = counts(t);
+    uint64_t who = __ballot(on);
     L cur;
-    cur.load(z + (size_t)(t < t1 ? t : t0) * p.R, on, p.E, l);
-    while (t - sub < t1) {  // uniform
-        const int n = t + kBalTokens;
-        const bool non = counts(n);
+    cur.load(z + (size_t)(on ? t : 0) * p.R, on, p.E, l);
+    int id = pair(t, who);
+    __syncthreads();
+    while (t - sub < p.T) {  // uniform
+        const int next = t + step;
+        const bool non = counts(next);
+        const uint64_t nwho = __ballot(non);
         L nxt;
-        nxt.load(z + (size_t)(n < t1 ? n : t0) * p.R, non, p.E, l);
-        float q[kI];
-        token_probs(cur, on, p.E, l, q);
+        nxt.load(z + (size_t)(non ? next : 0) * p.R, non, p.E, l);
+        const int nid = pair(next, nwho);
+        if (who) {  // uniform: padding costs nothing
+            float q[kI];
+            token_probs(cur, on, p.E, l, q);
 #pragma unroll
-        for (int i = 0; i < kI; ++i) acc[i] += q[i];
-        t = n;
+            for (int i = 0; i < kI; ++i) acc[i] += q[i];
+            if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
+            n += __popcll(who) / kRowLanes;
+        }
+        t = next;
         on = non;
+        who = nwho;
+        id = nid;
         cur = nxt;
     }
+    if (lane == 0) atomicAdd(&counted, n);
 #pragma unroll
     for (int i = 0; i < kI; ++i) {  // the wave's four tokens' lanes
         acc[i] += __uint_as_float(partner32<4>(__float_as_uint(acc[i])));
@@ -230,7 +239,16 @@ __global__ __launch_bounds__(4 * kMaxE) void balance_join_kernel(BalanceParams p
 // dlogits, 16 lanes a token; columns past the experts and tokens that do not count get 0.
 template <class Z, int kI, int kV>
 __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceBwdParams p) {
-    const int lane = lane_id(), l = lane & (kRowLanes - 1);
+    const int lane = lane_id(), l = lane & (kRowLanes - 1), per = 256 / kRowLanes;
+    const Z *z = reinterpret_cast<const Z *>(p.logits);
+    Z *dz = reinterpret_cast<Z *>(p.dlogits);
+    // the next token's logits on their way, the first while the counts come
+    using L = Logits<Z, kI, kV>;
+    auto counts = [&](int64_t t) { return t < p.T && (!p.mask || p.mask[t]); };
+    int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / kRowLanes;
+    bool on = counts(t);
+    L cur;
+    cur.load(z + (size_t)(t < p.T ? t : 0) * p.R, on, p.E, l);
     const int n = *p.tokens;
     float d[kI];
 #pragma unroll
@@ -239,34 +257,36 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceBwdParams 
         d[i] = e < p.E ? (float)((int64_t)p.counts[e] * p.E - (int64_t)kTopK * n) : 0.0f;
     }
     const float factor = n > 0 ? (float)((double)*p.dloss / ((double)kTopK * n * n)) : 0.0f;
-    const Z *z = reinterpret_cast<const Z *>(p.logits);
-    Z *dz = reinterpret_cast<Z *>(p.dlogits);
-    const int per = 256 / kRowLanes;
-    for (int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / kRowLanes; t - lane / kRowLanes < p.T;
-         t += (int64_t)gridDim.x * per) {
-        const bool there = t < p.T, on = there && (!p.mask || p.mask[t]);
-        float q[kI];
+    while (t - lane / kRowLanes < p.T) {  // uniform
+        const int64_t next = t + (int64_t)gridDim.x * per;
+        const bool there = t < p.T, non = counts(next);
+        L nxt;
+        nxt.load(z + (size_t)(next < p.T ? next : 0) * p.R, non, p.E, l);
         const size_t at = (size_t)(there ? t : 0) * p.R;
-        Logits<Z, kI, kV> raw;
-        raw.load(z + at, on, p.E, l);
-        token_probs(raw, on, p.E, l, q);
-        float mean = 0.0f;
+        float q[kI] = {}, mean = 0.0f;
+        if (__any(on)) {  // padding is only cleared
+            token_probs(cur, on, p.E, l, q);
 #pragma unroll
-        for (int i = 0; i < kI; ++i) mean = fmaf(q[i], d[i], mean);
-        mean = row_sum(mean);
-        if (!there) continue;
-#pragma unroll
-        for (int i = 0; i < kI; ++i) q[i] = on ? factor * (q[i] * (d[i] - mean)) : 0.0f;
-#pragma unroll
-        for (int i = 0; i < kI; i += kV) {
-            const int e = Logits<Z, kI, kV>::expert(i, l);
-            if (e + kV <= p.E) put_piece<kV>(dz + at + e, q + i);
-            else
-#pragma unroll
-                for (int k = 0; k < kV; ++k)
-                    if (e + k < p.E) put(dz + at + e + k, q[i + k]);
+            for (int i = 0; i < kI; ++i) mean = fmaf(q[i], d[i], mean);
+            mean = row_sum(mean);
         }
-        for (int c = p.E + l; c < p.R; c += kRowLanes) put(dz + at + c, 0.0f);
+        if (there) {
+#pragma unroll
+            for (int i = 0; i < kI; ++i) q[i] = on ? factor * (q[i] * (d[i] - mean)) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < kI; i += kV) {
+                const int e = L::expert(i, l);
+                if (e + kV <= p.E) put_piece<kV>(dz + at + e, q + i);
+                else
+#pragma unroll
+                    for (int k = 0; k < kV; ++k)
+                        if (e + k < p.E) put(dz + at + e + k, q[i + k]);
+            }
+            for (int c = p.E + l; c < p.R; c += kRowLanes) put(dz + at + c, 0.0f);
+        }
+        t = next;
+        on = non;
+        cur = nxt;
     }
 }
 
