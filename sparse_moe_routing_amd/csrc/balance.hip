@@ -250,12 +250,13 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceBwdParams 
     L cur;
     cur.load(z + (size_t)(t < p.T ? t : 0) * p.R, on, p.E, l);
     const int n = *p.tokens;
+    int c[kI];  // (without branches: all of them on their way at once)
+#pragma unroll
+    for (int i = 0; i < kI; ++i) c[i] = p.counts[min(L::expert(i, l), p.E - 1)];
     float d[kI];
 #pragma unroll
-    for (int i = 0; i < kI; ++i) {
-        const int e = Logits<Z, kI, kV>::expert(i, l);
-        d[i] = e < p.E ? (float)((int64_t)p.counts[e] * p.E - (int64_t)kTopK * n) : 0.0f;
-    }
+    for (int i = 0; i < kI; ++i)  // whole numbers below 2^53: rounded once
+        d[i] = L::expert(i, l) < p.E ? (float)((double)c[i] * p.E - (double)kTopK * n) : 0.0f;
     const float factor = n > 0 ? (float)((double)*p.dloss / ((double)kTopK * n * n)) : 0.0f;
     while (t - lane / kRowLanes < p.T) {  // uniform
         const int64_t next = t + (int64_t)gridDim.x * per;
