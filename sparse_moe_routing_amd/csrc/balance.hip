@@ -12,10 +12,10 @@
 //
 // All of them read or write the logits' array once and compute a few instructions per element: HBM
 // bounds them for large T, a launch and one dependent chain for small ones. Measured (us; loss and gradient
-// from Python one after the other): 192 tokens of 256 fp32 logits 17 (two launches), 8192 21.5 (three; 25 MB),
-// 131072 of bf16 logits in padded sequences 61. On the GPU, after the caches were filled with other data, the
-// latter is 25.6 for the sums (40 MB of the tokens that count; waits are 67 % of the waves' cycles), 7.6 for
-// joining them, 34.4 for the gradient (the same 37 MB again, 67 MB of stores).
+// from Python one after the other): 192 tokens of 256 fp32 logits 17 (two launches), 8192 20 to 22 (three; 25 MB),
+// 131072 of bf16 logits in padded sequences 51. On the GPU, after the caches were filled with other data, the
+// latter is 23 for the sums (38 MB of the tokens that count; waits are 66 % of the waves' cycles), 7.7 for
+// joining them, 28 for the gradient (the same 36 MB again, 67 MB of stores).
 #include "device_common.h"
 #include "kernels.h"
 #include "select_core.h"
@@ -135,7 +135,7 @@ __device__ __forceinline__ void write_loss(const BalanceParams &p, int e, double
 
 // A block's share of the tokens: sums of their probabilities and counts of their pairs. One block: the
 // loss at once; more: the block's row of the partial sums (balance_join_kernel adds them up in order). One block
-// takes up to 512 tokens: a second launch costs about what its eight passes do (7.6 us for the join on its own, 11.6 for
+// takes up to 512 tokens: a second launch costs about what its eight passes do (7.6 us for the join on its own, 11.2 for
 // the one block over 192 tokens). 16 lanes a token keep a token's sums within lane moves of one row of lanes, and a
 // block's 16 waves take 64 tokens a pass.
 template <class Z, int kI, int kV>
