@@ -268,7 +268,8 @@ int moe_matmul_i8(const int8_t *x, const float *x_scale, int32_t n_rows, const i
  * offsets and swiglu as for moe_matmul_i8 (gate rows first; silu(z[n][i]) z[n][I + i]); rows outside
  * [offsets[0], offsets[E]) are left as they were; offsets are clamped to [0, n_rows], and where they
  * fall y is unspecified, but nothing outside it is touched.
- * Sums are fp32 and y is rounded once to `y_dtype`. With fp32 x or fp32 y the codes, zero points and
+ * Sums are fp32 (their roundings are relative to scale |x| (code + 16) and scale |x| zero, also where
+ * the two cancel) and y is rounded once to `y_dtype`. With fp32 x or fp32 y the codes, zero points and
  * rows are multiplied as they are and the scales are applied in fp32. With bf16 x and bf16 y the same
  * holds for few rows; for many the weights scale (code - zero) are rounded to bf16, each by at most
  * 2^-8 of itself, so that z moves by at most 2^-8 sum |x w|. Which kernel runs, and with it the order

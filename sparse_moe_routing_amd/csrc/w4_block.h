@@ -20,7 +20,8 @@
 //   stands beside them, and 320 rows fit. The rounding moves a result by at most 2^-8 sum |x w|; with normal
 //   data by 0.0011 of its norm, where rounding the result itself takes 0.0017.
 // Measured (us): 8192 x 4096 x 4096 exact with the codes turned over by each multiplying wave 318, with one
-// conversion a block 281, rounded 257 to 285 on different cards (1070 to 965 TFLOP/s; a large bf16 library product of that shape reaches 1310).
+// conversion a block 281, rounded 257 to 285 on different cards (1070 to 965 TFLOP/s; a bf16 library product of that
+// shape reaches 1310).
 // 65536 rows over 256 experts of 2048 x 1024 rounded, 256 rows a block 408, 320 (all of most experts' rows) 332
 // to 357. Of the 281, by leaving work out: 234 without the loads of the rows, 261 without those of
 // the codes, 247 without the conversion, 189 without all three.
