@@ -269,13 +269,11 @@ int moe_matmul_i8(const int8_t *x, const float *x_scale, int32_t n_rows, const i
  * [offsets[0], offsets[E]) are left as they were; offsets are clamped to [0, n_rows], and where they
  * fall y is unspecified, but nothing outside it is touched.
  * Sums are fp32 (their roundings are relative to scale |x| (code + 16) and scale |x| zero, also where
- * the two cancel) and y is rounded once to `y_dtype`. With fp32 x or fp32 y the codes, zero points and
- * rows are multiplied as they are and the scales are applied in fp32. With bf16 x and bf16 y the same
- * holds for few rows; for many the weights scale (code - zero) are rounded to bf16, each by at most
- * 2^-8 of itself, so that z moves by at most 2^-8 sum |x w|. Which kernel runs, and with it the order
- * of the sums, is chosen from the sizes (rows of experts taken as spread evenly): the rest of a
- * batch, as long as it leaves the sizes alone, does not change a row's bits. 32 sum |x| over a group must stay in
- * fp32's range. A row that holds an infinity or a NaN gives NaN or an infinity in its own results
+ * the two cancel) and y is rounded once to `y_dtype`: rows, codes and zero points are multiplied as
+ * they are, and the scales are applied in fp32, whatever the types and however many rows there are. Which
+ * kernel runs, and with it the order of the sums, is chosen from the sizes (rows of experts taken as
+ * spread evenly): the rest of a batch, as long as it leaves the sizes alone, does not change a row's
+ * bits. 32 sum |x| over a group must stay in fp32's range. A row that holds an infinity or a NaN gives NaN or an infinity in its own results
  * only. n_rows: 0..8388608; E: 1..256; K: 32..16384, a multiple of the group; M: 8..65536, a
  * multiple of 8 (of 16 with swiglu). */
 int moe_matmul_w4(const void *x, int32_t n_rows, int32_t dtype, const uint8_t *w, const void *scale,

@@ -553,9 +553,8 @@ def matmul_w4(x, w, scale, zero=None, offsets=None, swiglu=False, dtype=None, y=
     with offsets[e] <= n < offsets[e + 1] (offsets [E + 1] int32 on the device; None: w holds one
     matrix for all rows). scale [E][K / G][M] fp32 or bf16 for groups of G = 32, 64 or 128 columns; zero
     [E][K / G][M] uint8, None: 8 for all. swiglu: w holds gate rows, then up rows, and y [n][M / 2] =
-    silu(gate) up. y of `dtype`, bf16 by default; rows of no expert keep what it held. Sums are fp32; with
-    bf16 x, bf16 y and many rows the weights are rounded to bf16 first (z moves by at most 2^-8 sum
-    |x w|), with fp32 x or y never. Records no gradient: operands that require one are refused."""
+    silu(gate) up. y of `dtype`, bf16 by default; rows of no expert keep what it held. Sums are fp32, and y
+    is rounded once. Records no gradient: operands that require one are refused."""
     import torch
     dev = x.device
     ctx = _switched(dev, stream)

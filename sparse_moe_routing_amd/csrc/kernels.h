@@ -226,7 +226,6 @@ hipError_t launch_matmul_w4(const W4Params &p, int x_dtype, hipStream_t s);
 // its kernel for many rows; tile_rows: a multiple of 64 up to 256
 hipError_t launch_w4_block_bf16(const W4Params &p, hipStream_t s);
 hipError_t launch_w4_block_f32(const W4Params &p, hipStream_t s);
-hipError_t launch_w4_block_round(const W4Params &p, hipStream_t s);  // bf16 rows, weights rounded to bf16
 
 // Element types: 0 fp32, 1 bf16.
 hipError_t launch_permute(const void *x, const int32_t *rows, int T, int H, int n_rows, int dtype,

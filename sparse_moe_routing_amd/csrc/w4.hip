@@ -1,10 +1,11 @@
 // w4.hip - products with 4-bit weights and a scale (and a zero point) per group of columns, grouped by
 // expert: y[n][m] = sum_g s[g][m] sum_{k in g} x[n][k] (c[m][k] - z[g][m]) for the rows n of expert e.
 //
-// In the form for few rows nothing is rounded on the way to the sums: a code is a whole number, exact in
+// Nothing is rounded on the way to the sums: a code is a whole number, exact in
 // bf16, and a bf16 row element is an operand as it stands; fp32 rows go in as three bf16 parts that add up to all
 // of their 24 bits. A group's sum runs in the matrix instructions (16x16x32, fp32 sums), the zero point and the
-// scale are applied to it in fp32: s (sum x (c - b) - (z - b) sum x), b a constant of the operand's form.
+// scale are applied to it in fp32: in the form for few rows as s (sum x (c - b) - (z - b) sum x), b a constant of
+// the operand's form.
 // Rows are the A operand and channels the B operand: a lane's accumulators are four rows of one
 // channel, so that one scale serves all of a lane's sums.
 // The form for many rows is in w4_block.h. Which one runs is chosen here, from estimated times.
@@ -367,8 +368,8 @@ Choice choose(const W4Params &p, int x_dtype, int cus) {
         if (nslab > 1) take(most(ceil(units / cus) * (5.0 + share * (wide ? 1.5 + 1.0 * k : 1.7 + 0.5 * k)), memory) + 2.0, {1 << k, 1, 0});
     }
     const int bcols = p.swiglu ? 128 : 256, SB = (Mo + bcols - 1) / bcols;
-    for (int rows = 64; rows <= (wide ? 128 : p.y_f32 ? 256 : 320); rows += 64) {
-        const double n = rows / 64, slab = wide ? 0.95 + 0.9 * n : p.y_f32 ? 0.9 + 0.4 * n : 0.85 + 0.27 * n;
+    for (int rows = 64; rows <= (wide ? 128 : 256); rows += 64) {
+        const double n = rows / 64, slab = wide ? 0.95 + 0.9 * n : 0.9 + 0.4 * n;
         const double unit = (p.K + 63) / 64 * slab + 1.5;
         take(most(ceil(likely_tiles(p, rows, 0.35) * SB / cus) * unit, memory) + 5.0, {0, 0, rows});
     }
@@ -385,7 +386,7 @@ hipError_t launch_matmul_w4(const W4Params &p, int x_dtype, hipStream_t s) {
         W4Params b = p;
         b.tile_rows = c.tile_rows;
         if (x_dtype == 0) return launch_w4_block_f32(b, s);
-        return p.y_f32 ? launch_w4_block_bf16(b, s) : launch_w4_block_round(b, s);
+        return launch_w4_block_bf16(b, s);
     }
     const int cols = swiglu ? kSCh / 2 : kSCh, S = (Mo + cols - 1) / cols;
     const long units = most_tiles(p, 4 * c.r) * S, room = (long)cus * kStreamBlocks;

@@ -1,30 +1,29 @@
 // w4_block.h - products with 4-bit weights for many rows (w4.hip has the arithmetic and the forms for
 // few).
 //
-// A block multiplies the rows of one expert, up to 320 of them, by 256 weight channels (with SwiGLU 128 gate
+// A block multiplies the rows of one expert, up to 256 of them, by 256 weight channels (with SwiGLU 128 gate
 // channels and the 128 up channels that go with them), 64 columns at a time: a slab. Rows are loaded
-// straight into LDS, whole cache lines, double-buffered. Codes come to registers, whole cache lines (or
-// halves) of several slabs at once, and each wave turns an eighth of a slab's into operands, which it puts into LDS for
+// straight into LDS, whole cache lines, double-buffered. Codes come to registers, whole cache lines of
+// four slabs at once, and each wave turns an eighth of a slab's into operands, which it puts into LDS for
 // all of them while the slab before is multiplied: every code is converted once per block.
 // Eight waves, two per SIMD: wave w takes the channels of half w % 2 and a quarter of the tile's 16-row
 // subtiles, at most kMaxN.
 //
+// Nothing is rounded on the way to the sums: an operand is the whole number code - zero (that / 16 without zero
+// points), and each group's sums are scaled in fp32, so that a row's results are as exact here as in the forms
+// for few rows. (Scales rounded into bf16 operands let the sums stay in the matrix instructions over all of K
+// and 320 rows fit a block: 257 us in place of the 281 below, 332 in place of the 525. But that moved a bf16
+// result by up to 2^-8 sum |x w|, and only where many rows came with it: 0.0026 of the norm after SwiGLU
+// in place of 0.0017.)
+//
 // Instructions bound it: a SIMD takes two vector instructions beside each matrix instruction of 16 cycles
-// for nothing, and every further one costs nearly its own time. Hence two forms.
-//   Exact (fp32 rows or results): an operand is the whole number code - zero (that / 16 without zero
-//   points), and each group's sums are scaled in fp32: with groups of 64 or more two vector instructions for
-//   each matrix instruction (four rows of a channel, two steps), the conversion on top. Up to 256 rows, 192 with
-//   zero points or fp32 scales, 128 of fp32 rows: what the registers hold.
-//   kRound (bf16 rows and results): an operand is scale (code - zero) rounded to bf16, as a layer of bf16
-//   weights would hold it, and the sums stay in the matrix instructions over all of K: the conversion is all that
-//   stands beside them, and 320 rows fit. The rounding moves a result by at most 2^-8 sum |x w|; with normal
-//   data by 0.0011 of its norm, where rounding the result itself takes 0.0017.
-// Measured (us): 8192 x 4096 x 4096 exact with the codes turned over by each multiplying wave 318, with one
-// conversion a block 281, rounded 257 to 285 on different cards (1070 to 965 TFLOP/s; a bf16 library product of that
-// shape reaches 1310).
-// 65536 rows over 256 experts of 2048 x 1024 rounded, 256 rows a block 408, 320 (all of most experts' rows) 332
-// to 357. Of the 281, by leaving work out: 234 without the loads of the rows, 261 without those of
-// the codes, 247 without the conversion, 189 without all three.
+// for nothing, and every further one costs nearly its own time. With groups of 64 or more the scaling is two
+// for each matrix instruction (four rows of a channel, two steps), the conversion comes on top. Up to 256 rows, 192
+// with zero points or fp32 scales, 128 of fp32 rows: what the registers hold.
+// Measured (us): 8192 x 4096 x 4096 with the codes turned over by each multiplying wave 318, with one
+// conversion a block 281 to 304 (of 281, by leaving work out: 234 without the loads of the rows, 261 without those of
+// the codes, 247 without the conversion, 189 without all three). 65536 rows over 256 experts of 2048 x 1024 with
+// SwiGLU 525.
 //
 // The blocks are persistent, one per CU: the last slab of a unit is multiplied, and its results are stored,
 // while the first slabs of the block's next unit load.
@@ -44,22 +43,21 @@ constexpr int kBA = kBCh / 2 / kTile;  // channel subtiles of a wave
 constexpr int kBK = 64;                // columns of a slab
 constexpr int kBS = kBK / kStepK;      // its steps
 
-template <class X, bool kGen, bool kRound>
+template <class X, bool kGen>
 struct W4Block {
     using F = Form<X>;
     static constexpr int kPer = F::kPer;                        // 128-byte pieces of a row in a slab
-    // row subtiles of a wave and rows of a block (registers: exact products with zero points need most)
-    static constexpr int kMaxN = kPer > 1 ? 2 : kRound ? 5 : kGen ? 3 : 4, kRows = 4 * kTile * kMaxN;
-    // slabs whose codes a wave loads at once: a cache line's, or half of one
-    static constexpr int kSub = kRound ? 2 : 4, kLineB = kSub * kBK / 2;
+    // row subtiles of a wave and rows of a block (registers: products with zero points need most)
+    static constexpr int kMaxN = kPer > 1 ? 2 : kGen ? 3 : 4, kRows = 4 * kTile * kMaxN;
+    static constexpr int kSub = 4, kLineB = kSub * kBK / 2;     // slabs whose codes a wave loads at once: a cache line's
     static constexpr int kXSegs = kRows / 8 / kBWaves;          // 1 KB segments of rows per wave and piece
     static constexpr int kGroupB = kGen ? 4 * kBCh : 2 * kBCh;  // bytes of a group's scales
     static constexpr int kPairGroups = 4;                       // most groups of two slabs
-    static constexpr int kScaleB = kRound ? 16 : kPairGroups * kGroupB;
-    static constexpr float kUnit = kGen || kRound ? 1.0f : 1.0f / 16.0f;  // of a code in the operands
+    static constexpr int kScaleB = kPairGroups * kGroupB;
+    static constexpr float kUnit = kGen ? 1.0f : 1.0f / 16.0f;  // of a code in the operands
 
     const W4Params &p;
-    int lane, wave, ch, th, cols, Mo, KB, gl, groups, slabg, sb;  // cols: output channels of a block
+    int lane, wave, ch, th, cols, Mo, KB, gl, groups, sb;  // cols: output channels of a block
     int nslab, nsuper;  // slabs, and slabs of whole lines of codes, in K
 
     __device__ __forceinline__ W4Block(const W4Params &p_) : p(p_) {
@@ -72,11 +70,9 @@ struct W4Block {
         KB = p.K / 2;
         gl = p.group == 128 ? 2 : p.group == 64 ? 1 : 0;
         groups = p.K / p.group;
-        slabg = 8 >> gl;
         sb = kGen && p.scale_f32 ? 4 : 2;
         nslab = (p.K + kBK - 1) / kBK;
         nsuper = (p.K + kSub * kBK - 1) / (kSub * kBK);
-        kept_read = spos(lane & 15, lane >> 4);
     }
     // The lane number, made anew: what is computed from it stays next to its use instead of in registers
     // across the products, which need them all.
@@ -85,11 +81,8 @@ struct W4Block {
         asm volatile("" : "+v"(l));
         return l;
     }
-    // Where the lane reads operands of a subtile's first step (the second: ^ 64), kept where there are registers
-    // for it, and where its own come in.
-    int kept_read;
+    // Where the lane reads operands of a subtile's first step (the second: ^ 64), and where its own come in.
     __device__ __forceinline__ int read_at() const {
-        if constexpr (kRound) return kept_read;
         const int l = here();
         return spos(l & 15, l >> 4);
     }
@@ -127,7 +120,7 @@ struct W4Block {
     // their zero points.
     struct Codes {
         uint4 c;
-        uint32_t z, s;
+        uint32_t z;
     };
     __device__ __forceinline__ void issue_c(const Unit &u, Codes (&c)[kSub], int S) const {
         const int l = here(), left = KB - S * kLineB, m = channel(32 * wave + (l >> 1));
@@ -148,46 +141,19 @@ struct W4Block {
                 c[h].z = bload1(rz, g < groups ? (uint32_t)(g * p.M + m) : kPast);
             }
         }
-        if constexpr (kRound) {
-            const size_t s_at = ((size_t)u.t.e * groups * p.M + u.m0) * sb;
-            const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(reinterpret_cast<const unsigned char *>(p.scale) + s_at,
-                                                          ((uint32_t)groups * (uint32_t)p.M - (uint32_t)u.m0) * sb);
-#pragma unroll
-            for (int h = 0; h < kSub; ++h) {
-                const int g = (2 * (kSub * S + h) + (l & 1)) >> gl, at = (g * p.M + m) * sb;
-                c[h].s = bload4(rs, g < groups ? (uint32_t)(at & ~3) : kPast);
-            }
-        }
     }
-    // What the lane's codes of a slab become operands with: codes' factor and what is added.
-    struct Factors {
-        float z, s;
-    };
-    __device__ __forceinline__ Factors factors(const Codes &c) const {
-        if constexpr (!kRound) return {kGen && p.zero ? 8.0f - (float)(int)c.z : 0.0f, 16.0f};
-        const float s = scale_of(c.s, channel(32 * wave + (here() >> 1)));
-        return {(p.zero ? -(float)(int)c.z : -8.0f) * s, 512.0f * s};
-    }
-    // Codes 4 half .. 4 half + 3 of a word as operands: whole numbers, or rounded with their scale. Whole numbers
-    // come from the conversion of signed 4-bit numbers (/ 16), one a code; where the scale is multiplied
-    // in, two at once from bytes 0..15 read as FP8 (E4M3: code 2^-9, exactly).
-    __device__ __forceinline__ void operands(uint32_t w, const Factors &k, int half, uint32_t (&o)[4]) const {
-        if constexpr (kRound) {
-            typedef float f32x2_t __attribute__((ext_vector_type(2)));
-            const uint32_t a = w & 0x0F0F0F0Fu, b = (w >> 4) & 0x0F0F0F0Fu;
-            const f32x2_t e = half ? __builtin_amdgcn_cvt_pk_f32_fp8((int)a, true) : __builtin_amdgcn_cvt_pk_f32_fp8((int)a, false);
-            const f32x2_t d = half ? __builtin_amdgcn_cvt_pk_f32_fp8((int)b, true) : __builtin_amdgcn_cvt_pk_f32_fp8((int)b, false);
-            o[2 * half] = pack_bf16(fmaf(e.x, k.s, k.z), fmaf(d.x, k.s, k.z));
-            o[2 * half + 1] = pack_bf16(fmaf(e.y, k.s, k.z), fmaf(d.y, k.s, k.z));
-        } else {
-            const uint32_t a = (w ^ 0x88888888u) >> (16 * half), b = a >> 4;
-            auto f = [&](uint32_t v) __attribute__((always_inline)) {
-                const float c = __builtin_amdgcn_cvt_off_f32_i4((int)v);
-                return __float_as_uint(kGen ? fmaf(c, k.s, k.z) : c);
-            };
-            o[2 * half] = halves(f(b & 0xFFu), f(a & 0xFFu), kHigh);
-            o[2 * half + 1] = halves(f((b >> 8) & 0xFFu), f((a >> 8) & 0xFFu), kHigh);
-        }
+    // What is added to the lane's codes of a slab (as signed numbers, times 16) with zero points.
+    __device__ __forceinline__ float offset(const Codes &c) const { return kGen && p.zero ? 8.0f - (float)(int)c.z : 0.0f; }
+    // Codes 4 half .. 4 half + 3 of a word as operands, whole numbers, from the conversion of signed 4-bit numbers
+    // (/ 16), one a code.
+    __device__ __forceinline__ void operands(uint32_t w, float z, int half, uint32_t (&o)[4]) const {
+        const uint32_t a = (w ^ 0x88888888u) >> (16 * half), b = a >> 4;
+        auto f = [&](uint32_t v) __attribute__((always_inline)) {
+            const float c = __builtin_amdgcn_cvt_off_f32_i4((int)v);
+            return __float_as_uint(kGen ? fmaf(c, 16.0f, z) : c);
+        };
+        o[2 * half] = halves(f(b & 0xFFu), f(a & 0xFFu), kHigh);
+        o[2 * half + 1] = halves(f((b >> 8) & 0xFFu), f((a >> 8) & 0xFFu), kHigh);
     }
     __device__ __forceinline__ uint32_t word(const Codes &c, int t) const { return t == 0 ? c.c.x : t == 1 ? c.c.y : t == 2 ? c.c.z : c.c.w; }
     // Piece t (0..3) of the lane's 32 operands of a slab, into LDS. (Written in assembly: before an LDS write
@@ -200,7 +166,7 @@ struct W4Block {
     __device__ __forceinline__ void convert(Codes c, unsigned char *ab) const {
         // (made anew: or the compiler does this work in front of the branch, for the waves that multiply too)
         asm volatile("" : "+v"(c.c.x), "+v"(c.c.y), "+v"(c.c.z), "+v"(c.c.w));
-        const Factors k = factors(c);
+        const float k = offset(c);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             uint32_t o[4];
@@ -266,7 +232,7 @@ struct W4Block {
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(scale[i & 1][g], sum[j][r], acc[i][j][r]);
         };
-        const Factors k = factors(c);
+        const float k = offset(c);
         uint32_t made[4];
         weights(0);
         bits(0);
@@ -316,61 +282,11 @@ struct W4Block {
 #pragma unroll
         for (int j = 0; j < kN; ++j) scaled(kBA - 1, kGroups - 1, j);
     }
-    // The same with the scales in the operands: the sums stay in the matrix instructions from slab to slab. A step
-    // after the other, so that 320 rows fit.
-    template <int kN>
-    __device__ __forceinline__ void slab_rounded(f32x4_t (&acc)[kBA][kN], const unsigned char *xb, const unsigned char *ab,
-                                                 const Codes &c, unsigned char *nab) const {
-        constexpr int kAll = kBS * kBA;
-        const int rd = read_at();
-        const unsigned char *mine = ab + ch * kBA * kTile * kSlabB, *rows = xb + th * kN * kTile * kSlabB;
-        const Factors k = factors(c);
-        uint4 x[kN], b[3];
-        uint32_t made[4];
-        auto weights = [&](int n) __attribute__((always_inline)) {
-            b[n % 3] = load16(mine + n % kBA * kTile * kSlabB + (rd ^ (64 * (n / kBA))));
-        };
-        auto row = [&](int j, int s) __attribute__((always_inline)) { return load16(rows + j * kTile * kSlabB + (rd ^ (64 * s))); };
-        // the second step's rows: in registers of their own where there are enough, or each as soon as the first
-        // step is done with its register
-        constexpr bool kRoom = kN < 5;
-        uint4 behind[kRoom ? kN : 1];
-        weights(0);
-#pragma unroll
-        for (int j = 0; j < kN; ++j) x[j] = row(j, 0);
-        weights(1);
-#pragma unroll
-        for (int n = 0; n < kAll; ++n) {
-            const int i = n % kBA;
-            if (kRoom && n == kBA)
-#pragma unroll
-                for (int j = 0; j < kN; ++j) x[j] = behind[j % (kRoom ? kN : 1)];
-            if (n + 2 < kAll) weights(n + 2);
-            if (kRoom && n >= kBA - kN && n < kBA) behind[(n - (kBA - kN)) % (kRoom ? kN : 1)] = row(n - (kBA - kN), 1);
-            if (n % 2 == 0) operands(word(c, n / 4), k, n / 2 % 2, made);
-            if (n % 4 == 3) store(nab, n / 4, made);
-#pragma unroll
-            for (int j = 0; j < kN; ++j) {
-                mma(acc[i][j], x[j], b[n % 3]);
-                if (!kRoom && n == kBA - 1) x[j] = row(j, 1);
-            }
-            // their order: the reads ahead first, then a few vector instructions before each matrix instruction
-            if (n + 2 < kAll) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            if (kRoom && n >= kBA - kN && n < kBA) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-#pragma unroll
-            for (int m = 0; m < kN; ++m) {
-                __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                if (!kRoom && n == kBA - 1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    }
 };
 
-template <class X, bool kGen, bool kRound>
+template <class X, bool kGen>
 __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(2, 2))) void w4_block_kernel(W4Params p) {
-    using B = W4Block<X, kGen, kRound>;
+    using B = W4Block<X, kGen>;
     // The buffers are separate objects, so that the compiler can tell loads into one from reads of the other.
     __shared__ __align__(16) unsigned char x0[B::kRows * B::kPer * kSlabB], x1[B::kRows * B::kPer * kSlabB], a0[kBCh * kSlabB], a1[kBCh * kSlabB];
     __shared__ __align__(16) unsigned char s0[B::kScaleB], s1[B::kScaleB];
@@ -405,7 +321,7 @@ __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(
     Unit u = unit(i);
     constexpr int kSub = B::kSub;
     typename B::Codes codes[kSub], ncodes[kSub];
-    if constexpr (!kRound) b.issue_s(u, s0, 0);
+    b.issue_s(u, s0, 0);
     b.issue_c(u, codes, 0);
     b.template issue_x<B::kXSegs>(u, x0, 0, true);
     b.convert(codes[0], a0);
@@ -430,22 +346,19 @@ __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(
                     const bool over = h == kSub - 1 && end;
                     if (over) b.template issue_x<B::kXSegs>(nxt, nxb, 0, more);
                     else b.template issue_x<kN>(u, nxb, s + 1, s + 1 < b.nslab);
-                    if (!kRound && h == 1) b.issue_s(u, s1, 2 * S + 1);
+                    if (h == 1) b.issue_s(u, s1, 2 * S + 1);
                     if (h == kSub - 2) b.issue_c(end ? nxt : u, ncodes, end ? 0 : S + 1);
-                    if (!kRound && h == 3) b.issue_s(end ? nxt : u, s0, end ? 0 : 2 * S + 2);
+                    if (h == 3) b.issue_s(end ? nxt : u, s0, end ? 0 : 2 * S + 2);
                     if (busy && s < b.nslab) {
-                        if constexpr (kRound) b.template slab_rounded<kN>(acc, xb, ab, c, nab);
-                        else b.template slab<kN, kFlush>(acc, xb, ab, sbuf, h, c, nab);
+                        b.template slab<kN, kFlush>(acc, xb, ab, sbuf, h, c, nab);
                     } else {
                         b.convert(c, nab);
                     }
                 };
                 turn(std::integral_constant<int, 0>{}, x0, x1, a0, a1, s0);
                 turn(std::integral_constant<int, 1>{}, x1, x0, a1, a0, s0);
-                if constexpr (kSub > 2) {
-                    turn(std::integral_constant<int, 2>{}, x0, x1, a0, a1, s1);
-                    turn(std::integral_constant<int, 3>{}, x1, x0, a1, a0, s1);
-                }
+                turn(std::integral_constant<int, 2>{}, x0, x1, a0, a1, s1);
+                turn(std::integral_constant<int, 3>{}, x1, x0, a1, a0, s1);
 #pragma unroll
                 for (int h = 0; h < kSub; ++h) codes[h] = ncodes[h];
             }
@@ -476,14 +389,11 @@ __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(
             else if (B::kMaxN == 2 || sub == 2) run(std::integral_constant<int, 2>{}, fc);
             else if constexpr (B::kMaxN > 2) {
                 if (B::kMaxN == 3 || sub == 3) run(std::integral_constant<int, 3>{}, fc);
-                else if constexpr (B::kMaxN > 3) {
-                    if (B::kMaxN == 4 || sub == 4) run(std::integral_constant<int, 4>{}, fc);
-                    else if constexpr (B::kMaxN > 4) run(std::integral_constant<int, 5>{}, fc);
-                }
+                else if constexpr (B::kMaxN > 3) run(std::integral_constant<int, 4>{}, fc);
             }
         };
-        if (kRound || b.gl > 0) sized(std::integral_constant<int, 2>{});
-        else if constexpr (!kRound) sized(std::integral_constant<int, 1>{});
+        if (b.gl > 0) sized(std::integral_constant<int, 2>{});
+        else sized(std::integral_constant<int, 1>{});
         if (!more) break;
         u = nxt;
     }
@@ -492,20 +402,20 @@ __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(
 
 }  // namespace
 
-template <class X, bool kRound>
+template <class X>
 static hipError_t launch_form(const W4Params &q, hipStream_t s) {
     auto go = [&](auto gen) {
         constexpr bool kGen = decltype(gen)::value;
-        constexpr int kRows = W4Block<X, kGen, kRound>::kRows;
+        constexpr int kRows = W4Block<X, kGen>::kRows;
         W4Params p = q;
         if (p.tile_rows > kRows) p.tile_rows = kRows;
         const int cus = num_cus(), Mo = p.swiglu ? p.M / 2 : p.M, cols = p.swiglu ? kBCh / 2 : kBCh;
         const long units = most_tiles(p, p.tile_rows) * ((Mo + cols - 1) / cols);
         const unsigned grid = (unsigned)((units < cus ? units : cus) + kXcds - 1) / kXcds * kXcds;
-        launch_k(w4_block_kernel<X, kGen, kRound>, grid, kBWaves * kWave, 0, s, p);
+        launch_k(w4_block_kernel<X, kGen>, grid, kBWaves * kWave, 0, s, p);
     };
-    if (kRound || q.zero || q.scale_f32) go(std::true_type{});
-    else if constexpr (!kRound) go(std::false_type{});
+    if (q.zero || q.scale_f32) go(std::true_type{});
+    else go(std::false_type{});
     return hipGetLastError();
 }
 

@@ -3,6 +3,6 @@
 
 namespace moe {
 
-hipError_t launch_w4_block_f32(const W4Params &p, hipStream_t s) { return launch_form<float, false>(p, s); }
+hipError_t launch_w4_block_f32(const W4Params &p, hipStream_t s) { return launch_form<float>(p, s); }
 
 }  // namespace moe
