@@ -70,12 +70,15 @@ class BalanceLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, ids, num_experts, mask):
         loss, counts, tokens = binding.balance_loss(logits, ids, num_experts, mask)
-        ctx.save_for_backward(logits, counts, tokens, mask)
+        # A copy: the caller may sum counts and tokens over ranks in place, and a collective does that
+        # without raising the version counter by which autograd would notice.
+        kept = torch.cat((counts, tokens.view(1)))
+        ctx.save_for_backward(logits, kept, mask)
         ctx.mark_non_differentiable(counts, tokens)
         return loss, counts, tokens
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dloss, dcounts, dtokens):
-        logits, counts, tokens, mask = ctx.saved_tensors
-        return binding.balance_loss_backward(dloss.contiguous(), logits, counts, tokens, mask), None, None, None
+        logits, kept, mask = ctx.saved_tensors
+        return binding.balance_loss_backward(dloss.contiguous(), logits, kept[:-1], kept[-1], mask), None, None, None

@@ -596,7 +596,8 @@ def balance_loss(logits, ids, num_experts=None, mask=None, stream=None):
     """(loss, counts [E] int32, tokens int32) of a routing: loss = E sum_e counts[e] / (8 tokens) mean_t P[t][e],
     P the softmax of the first E = num_experts (by default all) columns of logits [T][R] (fp32 or bf16),
     counts the pairs of ids [T][8] of each expert. mask [T] (bool or uint8): tokens with 0 do not
-    count. loss and tokens have no dimensions. The loss is differentiable in the logits."""
+    count. loss and tokens have no dimensions. The loss is differentiable in the logits; counts and tokens
+    are the caller's then too: what is written into them does not change the gradient."""
     import torch
     dev = logits.device
     ctx = _switched(dev, stream)
