@@ -204,6 +204,8 @@ class MoeLayer:
         are differentiable in given logits [T][R] (not in x); the logits returned are a copy that is
         not."""
         import torch
+        if x is None:
+            _no_tangent(logits)
         if logits is not None and x is None and logits.requires_grad and torch.is_grad_enabled():
             ctx = _switched(logits.device, stream)
             if ctx is not None:
@@ -317,7 +319,8 @@ class MoeLayer:
 # round's operators take a few microseconds each, so this side is kept short: no Stream object
 # (three microseconds) is made where nothing has to be switched. permute and unpermute are recorded by
 # autograd (autograd.py); the others give results without a gradient: 8-bit codes have none, and the
-# gradients' own operators are not differentiated again.
+# gradients' own operators are not differentiated again. Where a gradient is recorded or refused, a
+# forward-mode tangent is refused.
 _row_types = {}  # torch dtype -> the library's number (filled on first use)
 
 
@@ -360,6 +363,24 @@ def _switched(device, stream):
     return None
 
 
+_forward_ad = None  # torch.autograd.forward_ad (filled on first use)
+
+
+def _no_tangent(*operands):
+    """The operators have no forward-mode derivative: an operand (None: not given) that carries a tangent
+    is refused, which would be lost silently."""
+    global _forward_ad
+    if _forward_ad is None:
+        import torch.autograd.forward_ad
+        _forward_ad = torch.autograd.forward_ad
+    if _forward_ad._current_level < 0:  # no dual tensors at all
+        return
+    for t in operands:
+        if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError("an operand carries a forward-mode tangent, and the operators have no"
+                             " forward-mode derivative: detach it")
+
+
 def _recorded(out, name):
     """For a call whose operands require a gradient: whether one is recorded. A result buffer given
     by the caller is refused then, as by torch's own operators."""
@@ -380,6 +401,7 @@ def permute(x, rows, n_rows=None, xs=None, stream=None):
     if ctx is not None:
         with ctx:
             return permute(x, rows, n_rows, xs)
+    _no_tangent(x)
     if x.requires_grad and _recorded(xs, "xs"):
         from .autograd import Permute
         return Permute.apply(x, rows, n_rows)
@@ -436,6 +458,7 @@ def unpermute(ys, rows, w, shared=None, gate=None, dtype=None, y=None, stream=No
     if ctx is not None:
         with ctx:
             return unpermute(ys, rows, w, shared, gate, dtype, y)
+    _no_tangent(ys, w, shared, gate)
     if (ys.requires_grad or w.requires_grad or (shared is not None and shared.requires_grad) or
             (gate is not None and gate.requires_grad)) and _recorded(y, "y"):
         from .autograd import Unpermute
@@ -561,6 +584,7 @@ def matmul_w4(x, w, scale, zero=None, offsets=None, swiglu=False, dtype=None, y=
     if ctx is not None:
         with ctx:
             return matmul_w4(x, w, scale, zero, offsets, swiglu, dtype, y)
+    _no_tangent(x, scale)
     if (x.requires_grad or scale.requires_grad) and torch.is_grad_enabled():
         raise ValueError("matmul_w4 records no gradient: detach x and scale, or use torch.no_grad()")
     (n, K), (E, M, _), at = x.shape, w.shape, dev.index
@@ -604,6 +628,7 @@ def balance_loss(logits, ids, num_experts=None, mask=None, stream=None):
     if ctx is not None:
         with ctx:
             return balance_loss(logits, ids, num_experts, mask)
+    _no_tangent(logits)
     if logits.requires_grad and torch.is_grad_enabled():
         from .autograd import BalanceLoss
         return BalanceLoss.apply(logits, ids, num_experts, mask)
