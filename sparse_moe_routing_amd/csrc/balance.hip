@@ -4,8 +4,11 @@
 //   P[t] = softmax(z[t][0..E-1]);  c_e = pairs (t, k) with ids[t][k] = e;  N = counted tokens
 //   L = E sum_e (c_e / 8N) (1/N sum_t P[t][e])
 //   dL/dz[t][j] = E / N P[t][j] (f_j - sum_e f_e P[t][e]),  f_e = c_e / 8N
-// The shares of a nearly even routing are nearly 1 / E, and sum_e P = 1: the gradient is formed with
-// the whole numbers c_e E - 8N in place of f_e, so that nothing cancels in it.
+// sum_e P = 1, so that a number taken off all f_e changes nothing. The gradient is formed with the whole numbers d_e =
+// c_e - floor(8N / E) in place of f_e (the shares of a nearly even routing are nearly 1 / E), and for each token the
+// mean m = sum_e P d_e is taken off them, then what is left of it: P_j ((d_j - m) - sum_e P (d_e - m)). The
+// rounding of m cancels in that, and a token that is sure of expert j keeps its small d_j - m: with m taken off once, u |d_j| is
+// left in its place (a tenth of it at 1 - P_j = 1e-6).
 //
 //   w = softmax over the eight chosen logits, g = sigmoid(z[t][E]):
 //   dz[t][ids_k] = w_k (dw_k - sum_j w_j dw_j);  dz[t][E] = g (1 - g) dg;  0 elsewhere
@@ -256,26 +259,30 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceBwdParams 
 #pragma unroll
     for (int i = 0; i < kI; ++i) c[i] = p.counts[min(L::expert(i, l), p.E - 1)];
     float d[kI];
+    const double even = floor((double)kTopK * n / p.E);
 #pragma unroll
-    for (int i = 0; i < kI; ++i)  // whole numbers below 2^53: rounded once
-        d[i] = L::expert(i, l) < p.E ? (float)((double)c[i] * p.E - (double)kTopK * n) : 0.0f;
-    const float factor = n > 0 ? (float)((double)*p.dloss / ((double)kTopK * n * n)) : 0.0f;
+    for (int i = 0; i < kI; ++i)  // whole numbers, exact below 2^24
+        d[i] = L::expert(i, l) < p.E ? (float)((double)c[i] - even) : 0.0f;
+    const float factor = n > 0 ? (float)((double)*p.dloss * p.E / ((double)kTopK * n * n)) : 0.0f;
     while (t - lane / kRowLanes < p.T) {  // uniform
         const int64_t next = t + (int64_t)gridDim.x * per;
         const bool there = t < p.T, non = counts(next);
         L nxt;
         nxt.load(z + (size_t)(next < p.T ? next : 0) * p.R, non, p.E, l);
         const size_t at = (size_t)(there ? t : 0) * p.R;
-        float q[kI] = {}, mean = 0.0f;
+        float q[kI] = {}, mean = 0.0f, rest = 0.0f;
         if (__any(on)) {  // padding is only cleared
             token_probs(cur, on, p.E, l, q);
 #pragma unroll
             for (int i = 0; i < kI; ++i) mean = fmaf(q[i], d[i], mean);
             mean = row_sum(mean);
+#pragma unroll
+            for (int i = 0; i < kI; ++i) rest = fmaf(q[i], d[i] - mean, rest);
+            rest = row_sum(rest);
         }
         if (there) {
 #pragma unroll
-            for (int i = 0; i < kI; ++i) q[i] = on ? factor * (q[i] * (d[i] - mean)) : 0.0f;
+            for (int i = 0; i < kI; ++i) q[i] = on ? factor * (q[i] * ((d[i] - mean) - rest)) : 0.0f;
 #pragma unroll
             for (int i = 0; i < kI; i += kV) {
                 const int e = L::expert(i, l);
