@@ -223,7 +223,7 @@ hipError_t launch_balance(const BalanceParams &p, int dtype, hipStream_t s);
 hipError_t launch_balance_backward(const BalanceBwdParams &p, int dtype, hipStream_t s);
 hipError_t launch_select_backward(const SelectBwdParams &p, hipStream_t s);
 hipError_t launch_matmul_w4(const W4Params &p, int x_dtype, hipStream_t s);
-// its kernel for many rows; tile_rows: a multiple of 64 up to 256
+// its kernel for many rows; tile_rows: a multiple of 64 up to what the form's registers hold (w4_block_rows)
 hipError_t launch_w4_block_bf16(const W4Params &p, hipStream_t s);
 hipError_t launch_w4_block_f32(const W4Params &p, hipStream_t s);
 

@@ -9,8 +9,6 @@
 // Rows are the A operand and channels the B operand: a lane's accumulators are four rows of one
 // channel, so that one scale serves all of a lane's sums.
 // The form for many rows is in w4_block.h. Which one runs is chosen here, from estimated times.
-#include <math.h>
-
 #include "w4_core.h"
 
 namespace moe {
@@ -42,7 +40,7 @@ namespace {
 // (Against one 16 x 16 tile a wave with the rows loaded as they lie: one row 183 -> 45 us, 32 tokens over 256
 // experts 148 -> 36. Moving the sums between lanes in place of choosing among them takes 49 for the latter, two
 // tiles of 16 rows a wave spill.)
-constexpr int kSCh = 32;                   // weight channels of a wave
+constexpr int kSCh = kW4StreamChannels;    // weight channels of a wave
 constexpr int kSteps = kSlabK / kStepK;    // matrix instructions per 16 channels and slab
 constexpr int kCodeBytes = kSCh * kSlabB;  // a slab's codes
 constexpr int kScaleBytes = kWave * 16;    // room for its scales: at most 8 groups of 32 fp32 numbers
@@ -322,66 +320,13 @@ void launch_stream(const W4Params &p, bool swiglu, unsigned grid, hipStream_t s)
     else launch_k(w4_stream_kernel<X, false, kR, kKS, false>, grid, kKS * kWave, 0, s, p);
 }
 
-constexpr int kStreamBlocks = 8;  // one-wave blocks per CU (LDS)
-constexpr int kSplit = 8;         // waves that split K where there are few units
-
-// About how many row tiles of `per` rows there will be: the experts' counts are on the device, so even
-// routing is taken, and `more` of a tile more per expert.
-double likely_tiles(const W4Params &p, int per, double more) {
-    if (!p.offsets) return (p.n_rows + per - 1) / per;
-    const double experts = p.E < p.n_rows ? p.E : p.n_rows, each = p.n_rows / experts / per;
-    return experts * (each + more > 1.0 ? each + more : 1.0);
-}
-
-// Which kernel, and how it is cut, from estimates of all in us, with constants measured on MI355X (dense 4096
-// x 4096, groups of 128, one scale; here for 4-, 8- and 16-row waves of bf16 rows). A wave takes 1.1, 1.4 and 1.7 for
-// a slab of its stream alone on its CU; a CU takes a wave's slab every 0.21, 0.24 and 0.34. Eight waves
-// that split K take 5 and 1.7 to 2.7 for each slab of their eighth, one such block to a CU. A block's slab
-// of 64 columns costs 0.85 and 0.27 per 16-row subtile of a wave, its unit 1.5, its start 5. HBM gives 6 TB/s.
-// Measured where the choice turns (us; 4-, 8-, 16-row waves, blocks of 64, 128, 256 rows), dense 4096 x 4096: 32 rows
-// 28 (split), 15 (split), 10.9 (split), 75, 75, 75; 64 rows: 32, 29, 21 (split), 87, 86, 86; 256 rows: 105, 62, 47, 87,
-// 98, 119; 512 rows: 204, 114, 84, 86, 97, 120; 2048 rows: -, -, -, 169, 98, 120; 4096 rows: -, -, -, 342, 196, 131. 256 experts
-// of 2048 x 1024 with SwiGLU, even routing, 1 row an expert: 39, 45, 52, 108; 6 rows: 87, 72, 73, 150; 16 rows: 186,
-// 134, 123, 151; 32 rows: 343, 228, 192, 169; 64 rows: -, -, -, 248, 197, 197. 256 rows an expert: blocks of 256 rows
-// 408, of 320 (most experts' rows in one) 357.
-struct Choice {
-    int r, split, tile_rows;  // 4 r rows of a stream wave, split K or not; or r = 0: rows of a block
-};
-Choice choose(const W4Params &p, int x_dtype, int cus) {
-    const bool wide = x_dtype == 0;
-    const int Mo = p.swiglu ? p.M / 2 : p.M;
-    const double experts = p.offsets ? (p.E < p.n_rows ? p.E : p.n_rows) : 1;
-    const double weights = experts * p.M * p.K * (0.5 + (p.scale_f32 ? 4.0 : 2.0) / p.group);
-    const double memory = (weights + (double)p.n_rows * (p.K * (wide ? 4.0 : 2.0) + Mo * (p.y_f32 ? 4.0 : 2.0))) / 6e6;
-    auto most = [](double a, double b) { return a > b ? a : b; };
-    Choice c{0, 0, 256};
-    double best = 0;
-    auto take = [&](double us, const Choice &d) {
-        if (best == 0 || us < best) best = us, c = d;
-    };
-    const int cols = p.swiglu ? kSCh / 2 : kSCh, S = (Mo + cols - 1) / cols, nslab = (p.K + kSlabK - 1) / kSlabK;
-    static const double kAlone[2][3] = {{1.13, 1.4, 1.7}, {1.9, 2.3, 0.0}}, kEach[2][3] = {{0.21, 0.24, 0.34}, {0.39, 0.45, 0.0}};
-    for (int k = 0; k < (wide ? 2 : 3); ++k) {
-        const double units = likely_tiles(p, 4 << k, 0.6) * S, alone = kAlone[wide][k], busy = kEach[wide][k] * units / cus;
-        take(most(nslab * cbrt(alone * alone * alone + busy * busy * busy), memory) + 2.0, {1 << k, 0, 0});
-        const double share = (nslab + kSplit - 1) / kSplit;
-        if (nslab > 1) take(most(ceil(units / cus) * (5.0 + share * (wide ? 1.5 + 1.0 * k : 1.7 + 0.5 * k)), memory) + 2.0, {1 << k, 1, 0});
-    }
-    const int bcols = p.swiglu ? 128 : 256, SB = (Mo + bcols - 1) / bcols;
-    for (int rows = 64; rows <= (wide ? 128 : 256); rows += 64) {
-        const double n = rows / 64, slab = wide ? 0.95 + 0.9 * n : 0.9 + 0.4 * n;
-        const double unit = (p.K + 63) / 64 * slab + 1.5;
-        take(most(ceil(likely_tiles(p, rows, 0.35) * SB / cus) * unit, memory) + 5.0, {0, 0, rows});
-    }
-    return c;
-}
-
 }  // namespace
 
 hipError_t launch_matmul_w4(const W4Params &p, int x_dtype, hipStream_t s) {
     const bool swiglu = p.swiglu;
     const int Mo = swiglu ? p.M / 2 : p.M, cus = num_cus();
-    const Choice c = choose(p, x_dtype, cus);
+    const W4Choice c = w4_choose(W4Sizes{p.n_rows, p.E, p.M, p.K, p.group, p.offsets != nullptr, x_dtype == 0, p.scale_f32 != 0,
+                                         p.zero != nullptr, p.y_f32 != 0, swiglu}, cus);
     if (c.r == 0) {
         W4Params b = p;
         b.tile_rows = c.tile_rows;
@@ -389,13 +334,13 @@ hipError_t launch_matmul_w4(const W4Params &p, int x_dtype, hipStream_t s) {
         return launch_w4_block_bf16(b, s);
     }
     const int cols = swiglu ? kSCh / 2 : kSCh, S = (Mo + cols - 1) / cols;
-    const long units = most_tiles(p, 4 * c.r) * S, room = (long)cus * kStreamBlocks;
+    const long units = most_tiles(p, 4 * c.r) * S, room = (long)cus * kW4StreamBlocks;
     const long blocks = units <= room || c.split ? units : room;
     const unsigned grid = (unsigned)((blocks + kXcds - 1) / kXcds * kXcds);
     auto go = [&](auto x, auto rc) {
         using X = decltype(x);
         constexpr int kR = decltype(rc)::value;
-        if (c.split) launch_stream<X, kR, kSplit>(p, swiglu, grid, s);
+        if (c.split) launch_stream<X, kR, kW4Split>(p, swiglu, grid, s);
         else launch_stream<X, kR, 1>(p, swiglu, grid, s);
     };
     using R1 = std::integral_constant<int, 1>;

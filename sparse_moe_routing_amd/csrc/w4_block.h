@@ -48,7 +48,7 @@ struct W4Block {
     using F = Form<X>;
     static constexpr int kPer = F::kPer;                        // 128-byte pieces of a row in a slab
     // row subtiles of a wave and rows of a block (registers: products with zero points need most)
-    static constexpr int kMaxN = kPer > 1 ? 2 : kGen ? 3 : 4, kRows = 4 * kTile * kMaxN;
+    static constexpr int kRows = w4_block_rows(kPer > 1, kGen), kMaxN = kRows / (4 * kTile);
     static constexpr int kSub = 4, kLineB = kSub * kBK / 2;     // slabs whose codes a wave loads at once: a cache line's
     static constexpr int kXSegs = kRows / 8 / kBWaves;          // 1 KB segments of rows per wave and piece
     static constexpr int kGroupB = kGen ? 4 * kBCh : 2 * kBCh;  // bytes of a group's scales
@@ -403,20 +403,18 @@ __global__ __launch_bounds__(kBWaves *kWave) __attribute__((amdgpu_waves_per_eu(
 }  // namespace
 
 template <class X>
-static hipError_t launch_form(const W4Params &q, hipStream_t s) {
-    auto go = [&](auto gen) {
+static hipError_t launch_form(const W4Params &p, hipStream_t s) {
+    auto go = [&](auto gen) -> hipError_t {
         constexpr bool kGen = decltype(gen)::value;
         constexpr int kRows = W4Block<X, kGen>::kRows;
-        W4Params p = q;
-        if (p.tile_rows > kRows) p.tile_rows = kRows;
+        if (p.tile_rows < 1 || p.tile_rows > kRows) return hipErrorInvalidValue;  // the buffers hold no more
         const int cus = num_cus(), Mo = p.swiglu ? p.M / 2 : p.M, cols = p.swiglu ? kBCh / 2 : kBCh;
         const long units = most_tiles(p, p.tile_rows) * ((Mo + cols - 1) / cols);
         const unsigned grid = (unsigned)((units < cus ? units : cus) + kXcds - 1) / kXcds * kXcds;
         launch_k(w4_block_kernel<X, kGen>, grid, kBWaves * kWave, 0, s, p);
+        return hipGetLastError();
     };
-    if (q.zero || q.scale_f32) go(std::true_type{});
-    else go(std::false_type{});
-    return hipGetLastError();
+    return p.zero || p.scale_f32 ? go(std::true_type{}) : go(std::false_type{});
 }
 
 }  // namespace moe

@@ -4,6 +4,7 @@
 #include "device_common.h"
 #include "expert_tiles.h"
 #include "kernels.h"
+#include "w4_choice.h"
 
 namespace moe {
 
@@ -90,6 +91,7 @@ __device__ __forceinline__ uint4 all(uint32_t v) { return uint4{v, v, v, v}; }
 // A slab is a whole cache line of a channel's codes.
 constexpr int kSlabB = 128;                // bytes of a channel's codes in a slab
 constexpr int kSlabK = 2 * kSlabB;         // columns
+static_assert(kSlabK == kW4StreamColumns, "the choice counts these slabs");
 constexpr uint32_t kPast = 0xFFFFFFF0u;    // a buffer offset past every range
 
 // Position of 16-byte piece pc (0..7) of staged row r: rows 2m and 2m + 1 rotate by m, so that the 16 rows
