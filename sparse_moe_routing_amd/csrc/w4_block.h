@@ -12,7 +12,7 @@
 // Nothing is rounded on the way to the sums: an operand is the whole number code - zero (that / 16 without zero
 // points), and each group's sums are scaled in fp32, so that a row's results are as exact here as in the forms
 // for few rows. (Scales rounded into bf16 operands let the sums stay in the matrix instructions over all of K
-// and 320 rows fit a block: 257 us in place of the 281 below, 332 in place of the 525. But that moved a bf16
+// and 320 rows fit a block: 257 us in place of the 281 below, 332 in place of the 475. But that moved a bf16
 // result by up to 2^-8 sum |x w|, and only where many rows came with it: 0.0026 of the norm after SwiGLU
 // in place of 0.0017.)
 //
@@ -23,7 +23,7 @@
 // Measured (us): 8192 x 4096 x 4096 with the codes turned over by each multiplying wave 318, with one
 // conversion a block 281 to 304 (of 281, by leaving work out: 234 without the loads of the rows, 261 without those of
 // the codes, 247 without the conversion, 189 without all three). 65536 rows over 256 experts of 2048 x 1024 with
-// SwiGLU 525.
+// SwiGLU 472 to 480.
 //
 // The blocks are persistent, one per CU: the last slab of a unit is multiplied, and its results are stored,
 // while the first slabs of the block's next unit load.

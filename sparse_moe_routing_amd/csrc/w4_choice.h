@@ -20,25 +20,38 @@ constexpr int kW4Split = 8;            // waves that split K where there are few
 // The most rows of a block, a multiple of 64: what the registers hold. general: with zero points or fp32 scales.
 constexpr int w4_block_rows(bool x_f32, bool general) { return x_f32 ? 128 : general ? 192 : 256; }
 
-// About how many row tiles of `per` rows there will be: the experts' counts are on the device, so even
-// routing is taken, and `more` of a tile more per expert.
+// About how many row tiles of `per` rows there will be. The host does not have the experts' counts, so even routing
+// is taken. Waves of few rows: `more` of a tile more per expert.
 inline double w4_likely_tiles(const W4Sizes &p, int per, double more) {
     if (!p.grouped) return (p.n_rows + per - 1) / per;
     const double experts = p.E < p.n_rows ? p.E : p.n_rows, each = p.n_rows / experts / per;
     return experts * (each + more > 1.0 ? each + more : 1.0);
+}
+// Blocks: a whole tile of one expert is many units' time, and whether its count passes a multiple of `per` decides
+// it. The counts of an even routing scatter by their root: an expert has a tile k + 1 as often as its count
+// passes k per. (256 rows an expert, 2048 x 1024 with SwiGLU: nearly all have two tiles of 192 rows, half have two of 256: 531
+// and 478 us. With 0.35 of a tile more in place of this 192 rows were chosen.)
+inline double w4_block_tiles(const W4Sizes &p, int per) {
+    if (!p.grouped) return (p.n_rows + per - 1) / per;
+    const double mean = (double)p.n_rows / p.E, scatter = sqrt(mean);
+    if (scatter > per) return p.E * (mean / per + 0.5);  // any rest is as likely as any other
+    const double sure = floor((mean - 6.0 * scatter) / per);
+    double tiles = sure > 0 ? sure + 1.0 : 1.0 - exp(-mean);
+    for (int k = sure > 0 ? (int)sure + 1 : 1; k * per < mean + 6.0 * scatter; ++k)
+        tiles += 0.5 * erfc((k * per + 0.5 - mean) / (1.41421356 * scatter));
+    return p.E * tiles;
 }
 
 // Which kernel, and how it is cut, from estimates of all in us, with constants measured on MI355X (dense 4096
 // x 4096, groups of 128, one scale; here for 4-, 8- and 16-row waves of bf16 rows). A wave takes 1.1, 1.4 and 1.7 for
 // a slab of its stream alone on its CU; a CU takes a wave's slab every 0.21, 0.24 and 0.34. Eight waves
 // that split K take 5 and 1.7 to 2.7 for each slab of their eighth, one such block to a CU. A block's slab
-// of 64 columns costs 0.85 and 0.27 per 16-row subtile of a wave, its unit 1.5, its start 5. HBM gives 6 TB/s.
-// Measured where the choice turns (us; 4-, 8-, 16-row waves, blocks of 64, 128, 256 rows), dense 4096 x 4096: 32 rows
-// 28 (split), 15 (split), 10.9 (split), 75, 75, 75; 64 rows: 32, 29, 21 (split), 87, 86, 86; 256 rows: 105, 62, 47, 87,
-// 98, 119; 512 rows: 204, 114, 84, 86, 97, 120; 2048 rows: -, -, -, 169, 98, 120; 4096 rows: -, -, -, 342, 196, 131. 256 experts
-// of 2048 x 1024 with SwiGLU, even routing, 1 row an expert: 39, 45, 52, 108; 6 rows: 87, 72, 73, 150; 16 rows: 186,
-// 134, 123, 151; 32 rows: 343, 228, 192, 169; 64 rows: -, -, -, 248, 197, 197. 256 rows an expert: blocks of 256 rows
-// 408, of 320 (most experts' rows in one) 357.
+// of 64 columns costs 0.9 and 0.4 per 16-row subtile of a wave, its unit 1.5, its start 5. HBM gives 6 TB/s.
+// Measured where the choice turns (us; 4-, 8-, 16-row waves, blocks of 64, 128, 192, 256 rows), dense 4096 x 4096: 32 rows
+// 27, 16, 12 (all split), 62, 62, 62, 62; 64 rows: 30, 28, 21 (split), 75, 75, 76, 76; 256 rows: 99, 69, 51, 77, 99, 123, 147;
+// 512 rows: 191, 128, 91, 77, 100, 123, 149; 2048 rows blocks of 160, 107, 126, 150; 4096 rows 299, 199, 243, 154. 256 experts
+// of 2048 x 1024 with SwiGLU, even routing, 1 row an expert: 40, 47, 54, 104; 6 rows: 90, 74, 76, 145; 16 rows: 185,
+// 136, 123, 146; 32 rows: 350, 231, 192, 164; 64 rows blocks of 241, 212, 210, 212; 256 rows 707, 528, 528, 478.
 struct W4Choice {
     int r, split, tile_rows;  // 4 r rows of a stream wave, split K or not; or r = 0: rows of a block
 };
@@ -66,7 +79,7 @@ inline W4Choice w4_choose(const W4Sizes &p, int cus) {
     for (int rows = 64; rows <= w4_block_rows(wide, p.zero || p.scale_f32); rows += 64) {
         const double n = rows / 64, slab = wide ? 0.95 + 0.9 * n : 0.9 + 0.4 * n;
         const double unit = (p.K + 63) / 64 * slab + 1.5;
-        take(most(ceil(w4_likely_tiles(p, rows, 0.35) * SB / cus) * unit, memory) + 5.0, {0, 0, rows});
+        take(most(ceil(floor(w4_block_tiles(p, rows) + 0.5) * SB / cus) * unit, memory) + 5.0, {0, 0, rows});
     }
     return c;
 }
