@@ -68,3 +68,21 @@ def test_large_counts_are_quickly_estimated():
         for E in (1, 2, 8, 256):
             choose(n, E, 4096, 4096, 64)
     assert time.perf_counter() - t < 12 * 100e-6
+
+
+def test_block_cases_reach_every_block_instance():
+    """The GPU tests' cases go to blocks, and between them run every form, scale grouping, epilogue and number of
+    row subtiles per wave."""
+    from w4_block_cases import CASES, LARGE, tiles
+    seen = set()
+    for name, (counts, M, K, G, x, scale, zero, y, swiglu) in CASES.items():
+        kind, rows = choose(sum(counts), len(counts), M, K, G, len(counts) > 1, x, scale, zero, y, swiglu)[:2]
+        assert kind == "block", name
+        for n in tiles(counts, rows):
+            seen.add((x, zero or scale == "f32", G == 32, swiglu, -(-n // 64)))
+    want = {(x, general, g32, swiglu, n)
+            for x in ("bf16", "f32") for general in (False, True) for g32 in (False, True) for swiglu in (False, True)
+            for n in range(1, block_rows(x, "bf16", general) // 64 + 1)}
+    assert seen == want, sorted(want - seen)
+    for name, (n, E, M, K, G, grouped, kw) in LARGE.items():
+        assert choose(n, E, M, K, G, grouped, **kw)[0] == "block", name
