@@ -15,10 +15,11 @@
 //
 // All of them read or write the logits' array once and compute a few instructions per element: HBM
 // bounds them for large T, a launch and one dependent chain for small ones. Measured (us; loss and gradient
-// from Python one after the other): 192 tokens of 256 fp32 logits 17 (two launches), 8192 20 to 22 (three; 25 MB),
-// 131072 of bf16 logits in padded sequences 51. On the GPU, after the caches were filled with other data, the
-// latter is 23 for the sums (38 MB of the tokens that count; waits are 66 % of the waves' cycles), 7.7 for
-// joining them, 28 for the gradient (the same 36 MB again, 67 MB of stores).
+// from Python one after the other): 192 tokens of 256 fp32 logits 18 (two launches), 8192 22 to 23 (three; 25 MB),
+// 131072 of bf16 logits in padded sequences 54. On the GPU, after the caches were filled with other data, the
+// latter is 23 for the sums (38 MB of the tokens that count; waits are 66 % of the waves' cycles: a pass asks for its
+// logits when its mask has come back, two latencies behind each other), 7.6 for joining them, 30.6 for the
+// gradient (the same 36 MB again, 67 MB of stores).
 #include "device_common.h"
 #include "kernels.h"
 #include "select_core.h"
@@ -241,7 +242,7 @@ __global__ __launch_bounds__(4 * kMaxE) void balance_join_kernel(BalanceParams p
 
 // dlogits, 16 lanes a token; columns past the experts and tokens that do not count get 0. At most four blocks per
 // CU (what its registers hold at once), each walking its tokens: 131072 bf16 tokens with padding 27 us, with 2048
-// blocks 31, with 4096 41.
+// blocks 31, with 4096 41 (all before the mean was taken off twice, which takes 2 to 3).
 template <class Z, int kI, int kV>
 __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceBwdParams p) {
     const int lane = lane_id(), l = lane & (kRowLanes - 1), per = 256 / kRowLanes;

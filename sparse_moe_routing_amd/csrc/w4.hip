@@ -8,7 +8,7 @@
 // the operand's form.
 // Rows are the A operand and channels the B operand: a lane's accumulators are four rows of one
 // channel, so that one scale serves all of a lane's sums.
-// The form for many rows is in w4_block.h. Which one runs is chosen here, from estimated times.
+// The form for many rows is in w4_block.h. Which one runs is chosen in w4_choice.h, from estimated times.
 #include "w4_core.h"
 
 namespace moe {
@@ -17,9 +17,9 @@ namespace {
 
 // ------------------------------------------------------------------------- few rows per expert
 // With a few rows per expert the time is the one read of the weights: HBM bounds it. Measured (us, one
-// call over changing operands): 256 experts of 2048 x 1024 with 32 tokens' 256 rows 36 (178 MB, 5.0 TB/s), one
-// row of 4096 x 65536 with zero points 45 (147 MB, 3.3 TB/s: the loads wait beside the operands' instructions,
-// which are those of four rows), 4 rows of 2048 x 1024 8.4 and 32 rows of 4096 x 4096 10.1 (a launch and one chain
+// call over changing operands): 256 experts of 2048 x 1024 with 32 tokens' 256 rows 35 to 38 (178 MB, 5.0 TB/s), one
+// row of 4096 x 65536 with zero points 45 (147 MB, 3.3 TB/s: its 2048 units are eight to a CU, which holds seven of
+// their blocks, so that the last eighth runs by itself), 4 rows of 2048 x 1024 8.4 and 32 rows of 4096 x 4096 10.1 (a launch and one chain
 // of loads).
 //
 // A wave takes up to 4 kR rows of one
@@ -27,8 +27,11 @@ namespace {
 // channels' codes in slabs of 128 bytes (256 columns), whole cache lines loaded straight into its own
 // ring of slab buffers, with the slab's scales and zero points beside them. The rows come through
 // buffer loads into registers; rows past the tile's read as zero without a memory access.
-// One-wave blocks fill a CU's LDS, eight of them. They are persistent: a wave walks its units, and the ring takes the
-// next unit's first slabs while the last slabs and the results of the present one are worked on.
+// Eight one-wave blocks are launched for a CU, which its LDS holds at once; of those with a ring of four and zero points
+// or fp32 scales (21 KB each) it holds seven, and the last one's units follow when one of them has ended. They are
+// persistent: a wave walks its units, and the ring takes the next unit's first slabs while the last slabs and
+// the results of the present one are worked on. A unit takes whole turns of the ring: with K = 512 half of the slabs of a
+// ring of four, and a third of those of a ring of three, are zeros.
 // kKS waves make a block and split K between them (their sums join in LDS, in order) where there is so
 // little to stream that single waves would not cover the chip; each such block takes one unit.
 //

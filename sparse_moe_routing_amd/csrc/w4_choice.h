@@ -14,7 +14,7 @@ struct W4Sizes {
 
 constexpr int kW4StreamChannels = 32;  // weight channels of a stream wave
 constexpr int kW4StreamColumns = 256;  // columns of its slabs
-constexpr int kW4StreamBlocks = 8;     // one-wave blocks per CU (LDS)
+constexpr int kW4StreamBlocks = 8;     // one-wave blocks launched per CU
 constexpr int kW4Split = 8;            // waves that split K where there are few units
 
 // The most rows of a block, a multiple of 64: what the registers hold. general: with zero points or fp32 scales.

@@ -94,13 +94,11 @@ def test_infinities_stay_in_their_row(name):
             assert not bool(y[n].isfinite().any())
 
 
-@pytest.mark.parametrize("name", CASES)
+@pytest.mark.parametrize("name", [n for n, c in CASES.items() if len(c[0]) > 1])
 def test_rows_behind_the_last_are_not_read(name):
     """Rows of no expert that hold NaN, and a table that ends sooner: the other rows' bits stay."""
     torch = _torch()
     c = Case(name, 3)
-    if c.dense:
-        pytest.skip("all rows are the matrix's")
     clean = c.run(y=blank(c))
     x = c.x.clone()
     x[:BEFORE] = x[-AFTER:] = float("nan")
