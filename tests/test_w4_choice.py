@@ -61,13 +61,17 @@ def test_height_is_the_fastest_measured(sizes, times):
 
 
 def test_large_counts_are_quickly_estimated():
+    """A tenth of a millisecond a call at most, the best of several tries."""
     import time
     choose(8, 8, 64, 64, 64)
-    t = time.perf_counter()
-    for n in (100000, 1000000, 8388608):
-        for E in (1, 2, 8, 256):
-            choose(n, E, 4096, 4096, 64)
-    assert time.perf_counter() - t < 12 * 100e-6
+    best = 1.0
+    for _ in range(7):
+        t = time.perf_counter()
+        for n in (100000, 1000000, 8388608):
+            for E in (1, 2, 8, 256):
+                choose(n, E, 4096, 4096, 64)
+        best = min(best, time.perf_counter() - t)
+    assert best < 12 * 100e-6
 
 
 def test_block_cases_reach_every_block_instance():
